@@ -52,7 +52,8 @@ typedef enum {
   ETA_ERR_CUDA = 4,            /* a CUDA runtime call or launch failed */
   ETA_ERR_DEVICE_TIMEOUT = 5,  /* returned by eta_status_from_device() */
   ETA_ERR_NONFINITE = 6,       /* returned by eta_status_from_device() */
-  ETA_ERR_DEVICE_BOUNDS = 7    /* returned by eta_status_from_device(): checked build */
+  ETA_ERR_DEVICE_BOUNDS = 7,   /* returned by eta_status_from_device(): checked build */
+  ETA_ERR_NO_PAGE = 8          /* returned by eta_status_from_device(): pool exhausted */
 } eta_status_t;
 
 /* Bits OR-ed into *dev_status by the kernels. */
@@ -66,6 +67,9 @@ typedef enum {
    is printed (device printf) with its file and line.  A library defect, never an
    input error: the host-side checks refuse every input that could cause one. */
 #define ETA_DEVSTAT_BOUNDS 0x10
+#define ETA_DEVSTAT_NO_PAGE 0x20     /* the page pool ran out; the refused rows are unchanged */
+#define ETA_DEVSTAT_BAD_ROW 0x40     /* a row or page number out of range, repeated, or in a state
+                                        that the call does not take (see the call); skipped */
 
 typedef struct {
   int32_t B;      /* batch rows (decode queries) */
@@ -450,6 +454,178 @@ eta_status_t eta_selftest_wait_timeout(uint32_t wait_limit, const int32_t* never
 int32_t eta_build_checked(void);
 eta_status_t eta_selftest_bounds(int64_t index, int64_t extent, int32_t* dev_status,
                                  void* stream);
+
+/*
+ * Paged caches.  (No counterpart in the pages: what a serving loop needs around the
+ * decode.)  Keys and values live in two pools of pages, one page holding one KV block
+ * (blk tokens) of every KV head of one row:
+ *   K_pool, V_pool  bf16 [n_pages, Hkv, blk, d], 16-byte aligned
+ *   dims            B rows, T_max = the row capacity in tokens, so NB = T_max / blk
+ *                   is the number of page-table columns; n_pages is a call argument
+ * The bookkeeping is one int32 array `state` (device memory, 16-byte aligned) of
+ * eta_page_state_words(dims, n_pages) words, in sections each padded to 4 words:
+ *   header[8]        header[0] = free pages; the others are zero
+ *   lengths[B]       tokens of each row
+ *   table[B, NB]     page of block j of row b, -1 at and past the row's last block
+ *   ref[n_pages]     rows that hold the page (0 = free)
+ *   free_list[n_pages]  stack of the free pages, entries [0, header[0]), top last
+ * Every change is deterministic: the same calls give the same page numbers, so
+ * replicas and sequence shards that make the same calls keep the same tables, and a
+ * copy of `state` is a snapshot that can be copied back (pages written in between
+ * keep what was written).  A page with ref > 1 is shared and read-only; only whole
+ * pages are ever shared.  Pages are handed out in order: the k-th page that a call
+ * needs, counted over its rows (or pairs) and their blocks in ascending order, is the
+ * k-th from the top of the free list.  When the pool cannot serve every row of a call,
+ * the rows are served in order while the pages last (a row that needs none is always
+ * served): the others are left unchanged and ETA_DEVSTAT_NO_PAGE is latched.
+ *
+ * Calls on one state must be ordered (one stream, or events).  Scratch: `ws` of
+ * eta_page_workspace_size(dims, n_pages) bytes, 16-byte aligned, zero-filled once
+ * before its first use; calls sharing one workspace must not overlap on the GPU.
+ * Limits (else ETA_ERR_UNSUPPORTED): n_pages * Hkv * blk < 2^31.
+ */
+size_t eta_page_state_words(const eta_dims_t* dims, int32_t n_pages);
+size_t eta_page_workspace_size(const eta_dims_t* dims, int32_t n_pages);
+/* Word offsets of the sections of `state`: out[0..4] = header, lengths, table, ref,
+ * free_list (host array). */
+eta_status_t eta_page_state_offsets(const eta_dims_t* dims, int32_t n_pages, int64_t* out);
+
+/* eta_page_init -- an empty cache: every row empty, every page free (free_list[k] =
+ * n_pages - 1 - k, so that pages are handed out from 0 upwards). */
+eta_status_t eta_page_init(const eta_dims_t* dims, int32_t n_pages, int32_t* state,
+                           void* stream);
+
+/*
+ * eta_page_append -- writes new tokens behind every row's last one, taking pages as
+ * needed: one token a row in a decode step, a whole chunk in a prefill.  Row b gets
+ * tokens cu_new[b] .. cu_new[b+1] - 1 of k_new / v_new (none: the row is untouched).
+ * k_new, v_new  bf16 [n_new, Hkv, d], 16-byte aligned;  cu_new  int32 [B + 1]
+ * (device), ascending from 0 to n_new.
+ * dev_status: NO_PAGE as above; BAD_LENGTH (a row past T_max: left unchanged; cu_new not
+ * ascending inside [0, n_new]: nothing is appended); BAD_ROW (the row's partly filled
+ * last page is shared or out of range: left unchanged).
+ */
+eta_status_t eta_page_append(const eta_dims_t* dims, int32_t n_pages, int32_t* state,
+                             eta_bf16_t* K_pool, eta_bf16_t* V_pool, const eta_bf16_t* k_new,
+                             const eta_bf16_t* v_new, const int32_t* cu_new, int32_t n_new,
+                             void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * eta_page_fork -- row dst[i] becomes a copy of row src[i], for i in [0, n): it shares
+ * src's whole pages (ref + 1) and gets a page of its own with the tokens of src's
+ * partly filled last one, if there is one.  src, dst int32 [n] (device), n <= B.  One
+ * row may be the source of many pairs.  All pairs see the state before the call.
+ * dev_status: NO_PAGE; BAD_ROW (a row out of range, a dst that is not empty, or one
+ * that an earlier pair named already: that pair is skipped).
+ */
+eta_status_t eta_page_fork(const eta_dims_t* dims, int32_t n_pages, int32_t* state,
+                           eta_bf16_t* K_pool, eta_bf16_t* V_pool, const int32_t* src,
+                           const int32_t* dst, int32_t n, void* ws, size_t ws_bytes,
+                           int32_t* dev_status, void* stream);
+
+/*
+ * eta_page_free -- empties rows[0 .. n) (device, n <= B): every page they held loses
+ * one reference each, and pages that nobody holds any more are pushed onto the free
+ * list in descending order of their numbers.  An empty row, or a row named twice, is
+ * emptied once.  dev_status: BAD_ROW (a row out of range: skipped), BAD_BLOCK (a page
+ * of the table out of range or free already: skipped).
+ */
+eta_status_t eta_page_free(const eta_dims_t* dims, int32_t n_pages, int32_t* state,
+                           const int32_t* rows, int32_t n, void* ws, size_t ws_bytes,
+                           int32_t* dev_status, void* stream);
+
+/*
+ * eta_page_compact -- moves the pages in use to the numbers [0, n_live), n_live =
+ * n_pages - header[0], so that the pool's upper part can be handed back: the i-th page
+ * in use at or above n_live moves to the i-th free number below it (both ascending).
+ * Tables, references and the free list (free_list[k] = n_pages - 1 - k) follow; the
+ * old places keep their contents.  dev_status: BAD_BLOCK (header[0] does not agree
+ * with ref: nothing is changed).
+ */
+eta_status_t eta_page_compact(const eta_dims_t* dims, int32_t n_pages, int32_t* state,
+                              eta_bf16_t* K_pool, eta_bf16_t* V_pool, void* ws,
+                              size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * eta_page_copy -- copies page src[i] of both pools to page dst[i], i in [0, n)
+ * (device arrays); the bookkeeping is not touched.  dev_status: BAD_ROW (a page out of
+ * range, a dst that an earlier pair named already, or a dst that is the src of any
+ * pair: that pair is skipped).
+ */
+eta_status_t eta_page_copy(const eta_dims_t* dims, int32_t n_pages, eta_bf16_t* K_pool,
+                           eta_bf16_t* V_pool, const int32_t* src, const int32_t* dst,
+                           int32_t n, void* ws, size_t ws_bytes, int32_t* dev_status,
+                           void* stream);
+
+/*
+ * eta_paged_build_block_meta -- eta_build_block_meta for a paged cache: block j of row
+ * b is page table[b, j] (table int32 [B, NB], lengths int32 [B]: the sections of the
+ * state, or the caller's own).  The metadata are laid out by row and block as there,
+ * and are the same bits.  A block whose page is out of range gets zeros (count 0), and
+ * ETA_DEVSTAT_BAD_BLOCK is latched.
+ */
+eta_status_t eta_paged_build_block_meta(
+    const eta_dims_t* dims, int32_t n_pages, const eta_bf16_t* K_pool, const eta_bf16_t* V_pool,
+    const int32_t* table, const int32_t* lengths, int32_t blk_begin, int32_t blk_end,
+    eta_cent_format_t cent_format, void* cent, float* rmax, float* var, int32_t* cnt,
+    float* vsum, float* vardim, int32_t* dev_status, void* stream);
+
+/* Element type of an attention output. */
+typedef enum { ETA_OUT_F32 = 0, ETA_OUT_BF16 = 1 } eta_out_format_t;
+
+/*
+ * eta_paged_decode -- eta_decode (and eta_dense_decode) for a paged cache.
+ *   tau NULL:        no gate (T is ignored);  else gated as eta_decode
+ *   union_idx NULL:  every block of the row (union_cnt ignored, prune must be SKIP);
+ *                    else the blocks union_idx[b, g, 0 .. union_cnt[b, g])
+ * o: fp32 or bf16 [B, Hq, d] by o_format; lse fp32 [B, Hq].  The other arguments as
+ * eta_decode (prune, vsum and cnt included).  Always the tensor-core engine
+ * (eta_set_decode_engine does not apply).  ws: eta_decode_workspace_size(dims) bytes.
+ * dev_status: TIMEOUT, BAD_LENGTH, BAD_BLOCK (a block past the row's length, or a page
+ * out of range: skipped).
+ */
+eta_status_t eta_paged_decode(const eta_dims_t* dims, int32_t n_pages, const eta_bf16_t* q,
+                              const float* tau, const eta_bf16_t* K_pool,
+                              const eta_bf16_t* V_pool, const int32_t* table,
+                              const int32_t* lengths, const int32_t* union_idx,
+                              const int32_t* union_cnt, float T, float scale,
+                              eta_prune_t prune, const float* vsum, const int32_t* cnt,
+                              eta_out_format_t o_format, void* o, float* lse, void* ws,
+                              size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * eta_shared_decode -- decode attention over every key of every row (no pruning) for a
+ * batch whose rows share long prefixes, each prefix read once for all of its rows.
+ * Rows group_off[k] .. group_off[k+1] - 1 form group k (group_off int32 [n_groups + 1],
+ * ascending from 0 to B); their first prefix_len[k] tokens (int32 [n_groups]) are the
+ * same pages (as eta_page_fork leaves them).  For every row b and head h, with the gate
+ * of eta_decode when tau is given (T as there) and none when tau is NULL:
+ *   s_t = scale * q[b,h] . k_t,  t < lengths[b];   o, lse as eta_dense_decode
+ * prefix_len is rounded down to whole pages; a row shorter than that does not share
+ * and is read by itself, as is every row of a group of one.  The page numbers of the
+ * prefix come from the group's first row that is long enough: a row of the group whose
+ * table holds other pages there gets the group's keys, not its own.  Rows of length 0
+ * give o = 0, lse = -inf.
+ * The prefix of up to 256 (row, head) pairs of one KV head is one pass of 128 x 128
+ * tensor-core tiles (S = Q K^T, O += P V) over its keys, cut into equal shares of key
+ * tiles, one per SM; the rows' own keys are shares of the same kind.  bf16 output: the
+ * weights P are rounded to bf16 (a relative error of at most 2^-8, the output's own);
+ * fp32 output: P is the sum of two bf16 terms (2^-16).
+ * table, lengths, o_format, o, lse: as eta_paged_decode.
+ * ws: eta_shared_decode_workspace_size(dims, n_groups) bytes, 16-byte aligned, no
+ * initial contents.  1 <= n_groups <= B.
+ * dev_status: TIMEOUT, BAD_LENGTH (a length or prefix_len out of range: clamped), BAD_ROW
+ * (group_off not ascending from 0 to B: rows outside every group are read by
+ * themselves), BAD_BLOCK (a page out of range: its keys are skipped).
+ */
+size_t eta_shared_decode_workspace_size(const eta_dims_t* dims, int32_t n_groups);
+eta_status_t eta_shared_decode(const eta_dims_t* dims, int32_t n_pages, int32_t n_groups,
+                               const eta_bf16_t* q, const float* tau, const eta_bf16_t* K_pool,
+                               const eta_bf16_t* V_pool, const int32_t* table,
+                               const int32_t* lengths, const int32_t* group_off,
+                               const int32_t* prefix_len, float T, float scale,
+                               eta_out_format_t o_format, void* o, float* lse, void* ws,
+                               size_t ws_bytes, int32_t* dev_status, void* stream);
 
 /* Maps a device status word (read back by the caller) to a status code. */
 eta_status_t eta_status_from_device(int32_t dev_status);

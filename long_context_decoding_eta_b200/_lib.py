@@ -24,13 +24,15 @@ ETA_OK = 0
 STATUS_NAMES = {0: "ok", 1: "invalid argument", 2: "unsupported shape",
                 3: "workspace missing or too small", 4: "CUDA error",
                 5: "device wait timed out", 6: "non-finite query",
-                7: "out-of-range index (checked build)"}
+                7: "out-of-range index (checked build)", 8: "page pool exhausted"}
 BOUND = {"exact": 0, "prob": 1, "prob_dim": 2}
 CENT = {"f32": 0, "bf16": 1}
 PRUNE = {"skip": 0, "floor": 1}
 TAIL_BLOCK = -1
 DEVSTAT_TIMEOUT, DEVSTAT_NONFINITE_Q, DEVSTAT_BAD_BLOCK, DEVSTAT_BAD_LENGTH = 1, 2, 4, 8
 DEVSTAT_BOUNDS = 0x10
+DEVSTAT_NO_PAGE, DEVSTAT_BAD_ROW = 0x20, 0x40
+OUT = {torch.float32: 0, torch.bfloat16: 1}
 
 EXPORTS = ("eta_build_block_meta", "eta_predict_tau", "eta_screen_workspace_size",
            "eta_screen", "eta_decode_workspace_size", "eta_decode", "eta_dense_decode",
@@ -41,7 +43,10 @@ EXPORTS = ("eta_build_block_meta", "eta_predict_tau", "eta_screen_workspace_size
            "eta_append_and_predict_tau", "eta_screen_launches", "eta_decode_launches",
            "eta_set_prefill_kernel", "eta_get_prefill_kernel", "eta_prefill_kernel_for",
            "eta_build_checked", "eta_selftest_bounds", "eta_set_screen_engine",
-           "eta_get_screen_engine")
+           "eta_get_screen_engine", "eta_page_state_words", "eta_page_workspace_size",
+           "eta_page_state_offsets", "eta_page_init", "eta_page_append", "eta_page_fork",
+           "eta_page_free", "eta_page_compact", "eta_page_copy", "eta_paged_build_block_meta",
+           "eta_paged_decode", "eta_shared_decode_workspace_size", "eta_shared_decode")
 ENGINE = {"auto": 0, "tcgen05": 1, "fma": 2}
 PREFILL_KERNEL = {"auto": 0, "one_tile": 1, "two_tile": 2}
 
@@ -137,6 +142,27 @@ def lib() -> C.CDLL:
     L.eta_build_checked.restype = I32
     L.eta_selftest_bounds.argtypes = [C.c_int64, C.c_int64, P, P]
     L.eta_selftest_bounds.restype = I32
+    SZ = C.c_size_t
+    for name, args in (
+            ("eta_page_state_offsets", [DIMS, I32, P]),
+            ("eta_page_init", [DIMS, I32, P, P]),
+            ("eta_page_append", [DIMS, I32, P, P, P, P, P, P, I32, P, SZ, P, P]),
+            ("eta_page_fork", [DIMS, I32, P, P, P, P, P, I32, P, SZ, P, P]),
+            ("eta_page_free", [DIMS, I32, P, P, I32, P, SZ, P, P]),
+            ("eta_page_compact", [DIMS, I32, P, P, P, P, SZ, P, P]),
+            ("eta_page_copy", [DIMS, I32, P, P, P, P, I32, P, SZ, P, P]),
+            ("eta_paged_build_block_meta", [DIMS, I32, P, P, P, P, I32, I32, I32, P, P, P, P, P,
+                                            P, P, P]),
+            ("eta_paged_decode", [DIMS, I32, P, P, P, P, P, P, P, P, F32, F32, I32, P, P, I32,
+                                  P, P, P, SZ, P, P]),
+            ("eta_shared_decode", [DIMS, I32, I32, P, P, P, P, P, P, P, P, F32, F32, I32, P, P,
+                                   P, SZ, P, P])):
+        getattr(L, name).argtypes = args
+        getattr(L, name).restype = I32
+    for name in ("eta_page_state_words", "eta_page_workspace_size",
+                 "eta_shared_decode_workspace_size"):
+        getattr(L, name).argtypes = [DIMS, I32]
+        getattr(L, name).restype = SZ
     for name in ("eta_build_block_meta", "eta_predict_tau", "eta_screen", "eta_decode",
                  "eta_dense_decode", "eta_calibrate_const_tau", "eta_status_from_device"):
         getattr(L, name).restype = I32
@@ -364,3 +390,98 @@ def eta_prefill(dims: Dims, Q, tau, K, V, lengths, T, scale, O, lse, dev_status=
     _check("eta_prefill", lib().eta_prefill(
         C.byref(dims), _p(Q), _p(tau), _p(K), _p(V), _p(lengths), float(T), float(scale), _p(O),
         _p(lse), _p(dev_status), _stream(stream)))
+
+
+# -- paged caches ---------------------------------------------------------------------
+def _bytes(ws) -> int:
+    return 0 if ws is None else ws.numel() * ws.element_size()
+
+
+def eta_page_state_words(dims: Dims, n_pages: int) -> int:
+    return int(lib().eta_page_state_words(C.byref(dims), int(n_pages)))
+
+
+def eta_page_workspace_size(dims: Dims, n_pages: int) -> int:
+    return int(lib().eta_page_workspace_size(C.byref(dims), int(n_pages)))
+
+
+def eta_page_state_offsets(dims: Dims, n_pages: int):
+    """Word offsets of (header, lengths, table, ref, free_list) in the state array."""
+    out = (C.c_int64 * 5)()
+    _check("eta_page_state_offsets", lib().eta_page_state_offsets(C.byref(dims), int(n_pages),
+                                                                  out))
+    return tuple(int(x) for x in out)
+
+
+def eta_page_init(dims: Dims, n_pages: int, state, stream=None):
+    _check("eta_page_init", lib().eta_page_init(C.byref(dims), int(n_pages), _p(state),
+                                                _stream(stream)))
+
+
+def eta_page_append(dims: Dims, n_pages: int, state, K_pool, V_pool, k_new, v_new, cu_new,
+                    n_new: int, ws, dev_status=None, stream=None):
+    _check("eta_page_append", lib().eta_page_append(
+        C.byref(dims), int(n_pages), _p(state), _p(K_pool), _p(V_pool), _p(k_new), _p(v_new),
+        _p(cu_new), int(n_new), _p(ws), _bytes(ws), _p(dev_status), _stream(stream)))
+
+
+def eta_page_fork(dims: Dims, n_pages: int, state, K_pool, V_pool, src, dst, n: int, ws,
+                  dev_status=None, stream=None):
+    _check("eta_page_fork", lib().eta_page_fork(
+        C.byref(dims), int(n_pages), _p(state), _p(K_pool), _p(V_pool), _p(src), _p(dst), int(n),
+        _p(ws), _bytes(ws), _p(dev_status), _stream(stream)))
+
+
+def eta_page_free(dims: Dims, n_pages: int, state, rows, n: int, ws, dev_status=None,
+                  stream=None):
+    _check("eta_page_free", lib().eta_page_free(
+        C.byref(dims), int(n_pages), _p(state), _p(rows), int(n), _p(ws), _bytes(ws),
+        _p(dev_status), _stream(stream)))
+
+
+def eta_page_compact(dims: Dims, n_pages: int, state, K_pool, V_pool, ws, dev_status=None,
+                     stream=None):
+    _check("eta_page_compact", lib().eta_page_compact(
+        C.byref(dims), int(n_pages), _p(state), _p(K_pool), _p(V_pool), _p(ws), _bytes(ws),
+        _p(dev_status), _stream(stream)))
+
+
+def eta_page_copy(dims: Dims, n_pages: int, K_pool, V_pool, src, dst, n: int, ws,
+                  dev_status=None, stream=None):
+    _check("eta_page_copy", lib().eta_page_copy(
+        C.byref(dims), int(n_pages), _p(K_pool), _p(V_pool), _p(src), _p(dst), int(n), _p(ws),
+        _bytes(ws), _p(dev_status), _stream(stream)))
+
+
+def eta_paged_build_block_meta(dims: Dims, n_pages: int, K_pool, V_pool, table, lengths,
+                               blk_begin, blk_end, cent, rmax, var, cnt, vsum=None,
+                               dev_status=None, stream=None, vardim=None):
+    _check("eta_paged_build_block_meta", lib().eta_paged_build_block_meta(
+        C.byref(dims), int(n_pages), _p(K_pool), _p(V_pool), _p(table), _p(lengths),
+        int(blk_begin), int(blk_end), _cent_format(cent), _p(cent), _p(rmax), _p(var), _p(cnt),
+        _p(vsum), _p(vardim), _p(dev_status), _stream(stream)))
+
+
+def eta_paged_decode(dims: Dims, n_pages: int, q, tau, K_pool, V_pool, table, lengths,
+                     union_idx, union_cnt, T, scale, prune, vsum, cnt, o, lse, ws,
+                     dev_status=None, stream=None):
+    """o's dtype (fp32 or bf16) selects the output format."""
+    _check("eta_paged_decode", lib().eta_paged_decode(
+        C.byref(dims), int(n_pages), _p(q), _p(tau), _p(K_pool), _p(V_pool), _p(table),
+        _p(lengths), _p(union_idx), _p(union_cnt), float(T), float(scale),
+        PRUNE[prune] if isinstance(prune, str) else int(prune), _p(vsum), _p(cnt), OUT[o.dtype],
+        _p(o), _p(lse), _p(ws), _bytes(ws), _p(dev_status), _stream(stream)))
+
+
+def eta_shared_decode_workspace_size(dims: Dims, n_groups: int) -> int:
+    return int(lib().eta_shared_decode_workspace_size(C.byref(dims), int(n_groups)))
+
+
+def eta_shared_decode(dims: Dims, n_pages: int, n_groups: int, q, tau, K_pool, V_pool, table,
+                      lengths, group_off, prefix_len, T, scale, o, lse, ws, dev_status=None,
+                      stream=None):
+    """o's dtype (fp32 or bf16) selects the output format."""
+    _check("eta_shared_decode", lib().eta_shared_decode(
+        C.byref(dims), int(n_pages), int(n_groups), _p(q), _p(tau), _p(K_pool), _p(V_pool),
+        _p(table), _p(lengths), _p(group_off), _p(prefix_len), float(T), float(scale),
+        OUT[o.dtype], _p(o), _p(lse), _p(ws), _bytes(ws), _p(dev_status), _stream(stream)))

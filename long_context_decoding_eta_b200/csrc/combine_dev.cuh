@@ -23,7 +23,7 @@ struct CombineParams {
   const float* vsum;
   const float* part_o;
   const float* part_ml;
-  float* o;
+  void* o;           // fp32, or bf16 (the kernel's output type)
   float* lse;
   int32_t* status;   // the checked build's range reports (may be NULL)
 };
@@ -134,13 +134,16 @@ ETA_DEV void combine_merge(const float* part_ml, const float* part_o, int r, int
 
 // o[oh] = O / L and lse[oh] = M + log L; an empty softmax (L = 0) gives o = 0,
 // lse = -inf.
-template <int D>
-ETA_DEV void combine_store(float* o, float* lse, size_t oh, int dd, float M, float L, float Oh) {
+ETA_DEV void store_out(float* p, float v) { *p = v; }
+ETA_DEV void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+template <int D, typename OutT>
+ETA_DEV void combine_store(OutT* o, float* lse, size_t oh, int dd, float M, float L, float Oh) {
   if (L > 0.f) {
-    o[oh * D + dd] = Oh / L;
+    store_out(o + oh * D + dd, Oh / L);
     if (dd == 0) lse[oh] = M + logf(L);
   } else {
-    o[oh * D + dd] = 0.f;
+    store_out(o + oh * D + dd, 0.f);
     if (dd == 0) lse[oh] = -INFINITY;
   }
 }

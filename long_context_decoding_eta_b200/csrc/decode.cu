@@ -30,6 +30,7 @@
 #include "decode_tc.cuh"
 #include "eta_common.cuh"
 #include "eta_host.h"
+#include "paged_host.h"
 #include "tma_host.h"
 
 namespace eta {
@@ -428,7 +429,7 @@ plan_kernel(int R, int Hkv, int NB, int blk, int T_max, const int32_t* __restric
 
 // One CTA per (row, KV head), thread = dim: merges the row's partial slots
 // (combine_merge), then in FLOOR mode adds the pruned blocks' keys with logit 0.
-template <int D, int G>
+template <int D, int G, typename OutT = float>
 __global__ void __launch_bounds__(D) combine_kernel(const CombineParams p) {
   ETA_PDL_ENTRY();
   extern __shared__ uint32_t adm[];     // FLOOR mode: admitted-block bitmap of the row
@@ -480,7 +481,8 @@ __global__ void __launch_bounds__(D) combine_kernel(const CombineParams p) {
       L = L * a + (float)nfloor * e0;
       M = Mf;
     }
-    combine_store<D>(p.o, p.lse, (size_t)b * p.Hq + (size_t)g * G + h, dd, M, L, Oh);
+    combine_store<D>(static_cast<OutT*>(p.o), p.lse, (size_t)b * p.Hq + (size_t)g * G + h, dd,
+                     M, L, Oh);
   }
 }
 
@@ -535,12 +537,14 @@ eta_status_t launch_decode(const eta_dims_t* dims, const DecodeParams& prm, int 
 }
 
 inline eta_status_t launch_combine(const eta_dims_t* dims, const CombineParams& cp,
-                                   cudaStream_t s) {
+                                   cudaStream_t s, bool bf16_out = false) {
   const int G = dims->Hq / dims->Hkv, R = dims->B * dims->Hkv;
   const size_t smem = cp.floor_mode ? (size_t)((num_blocks(dims) + 31) / 32) * 4 : 0;
-#define ETA_CMB_CASE(DD, GG)                                              \
-  if (dims->d == DD && G == GG)                                           \
-    return launch_k(combine_kernel<DD, GG>, dim3(R), dim3(DD), smem, s, cp);
+#define ETA_CMB_CASE(DD, GG)                                                                  \
+  if (dims->d == DD && G == GG)                                                               \
+    return bf16_out                                                                           \
+               ? launch_k(combine_kernel<DD, GG, __nv_bfloat16>, dim3(R), dim3(DD), smem, s, cp) \
+               : launch_k(combine_kernel<DD, GG>, dim3(R), dim3(DD), smem, s, cp);
   ETA_CMB_CASE(128, 1) ETA_CMB_CASE(128, 2) ETA_CMB_CASE(128, 4) ETA_CMB_CASE(128, 8)
   ETA_CMB_CASE(64, 1) ETA_CMB_CASE(64, 2) ETA_CMB_CASE(64, 4) ETA_CMB_CASE(64, 8)
 #undef ETA_CMB_CASE
@@ -607,6 +611,8 @@ eta_status_t launch_tc(const eta_dims_t* dims, const DecodeParams& d, const eta_
   prm.counts = counts;
   prm.row_off_g = const_cast<int32_t*>(d.row_off);   // the workspace
   prm.plan_g = const_cast<int32_t*>(d.plan);
+  prm.table = nullptr;
+  prm.n_pages = 0;
   const bool d64 = dims->d == 64;
   switch (dims->Hq / dims->Hkv) {
     case 1: return d64 ? launch_tc_t<1, DENSE, 64>(mk, mv, mq, prm, P, plan_in, s)
@@ -726,6 +732,110 @@ extern "C" eta_status_t eta_dense_decode(const eta_dims_t* dims, const eta_bf16_
   return run_decode<true>(dims, q, nullptr, K, V, lengths, nullptr, nullptr, 0.f, scale,
                           ETA_PRUNE_SKIP, nullptr, nullptr, o, lse, ws, ws_bytes, dev_status,
                           stream);
+}
+
+// ---------------------------------------------------------------- decode of a paged cache
+//
+// The tensor-core decode with its blocks behind the page table (decode_paged_kernel): the
+// same shares, partial slots and combine as the contiguous decode, one table lookup per
+// block on the TMA warp, two positions ahead of its use.  Bound by HBM like it.
+namespace eta {
+
+template <int G, bool GATE, int DD, int NS>
+eta_status_t launch_paged_t(const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mq,
+                            const tc::TcParams& prm, int P, cudaStream_t s) {
+  constexpr int smem = NS * G <= 16 ? tc::SMEM_BYTES : tc::SMEM_BYTES_WIDE;
+  if (!set_smem_once<tc::decode_paged_kernel<G, GATE, DD, NS>>(smem)) return ETA_ERR_CUDA;
+  return launch_k(tc::decode_paged_kernel<G, GATE, DD, NS>, dim3(P), dim3(tc::NT), smem, s, mk,
+                  mv, mq, prm);
+}
+
+template <int G>
+eta_status_t launch_paged_g(bool gate, bool d64, bool wide, const CUtensorMap& mk,
+                            const CUtensorMap& mv, const CUtensorMap& mq,
+                            const tc::TcParams& prm, int P, cudaStream_t s) {
+  switch ((gate ? 4 : 0) + (d64 ? 2 : 0) + (wide ? 1 : 0)) {
+    case 0: return launch_paged_t<G, false, 128, 2>(mk, mv, mq, prm, P, s);
+    case 1: return launch_paged_t<G, false, 128, 3>(mk, mv, mq, prm, P, s);
+    case 2: return launch_paged_t<G, false, 64, 2>(mk, mv, mq, prm, P, s);
+    case 3: return launch_paged_t<G, false, 64, 3>(mk, mv, mq, prm, P, s);
+    case 4: return launch_paged_t<G, true, 128, 2>(mk, mv, mq, prm, P, s);
+    case 5: return launch_paged_t<G, true, 128, 3>(mk, mv, mq, prm, P, s);
+    case 6: return launch_paged_t<G, true, 64, 2>(mk, mv, mq, prm, P, s);
+    default: return launch_paged_t<G, true, 64, 3>(mk, mv, mq, prm, P, s);
+  }
+}
+
+}  // namespace eta
+
+extern "C" eta_status_t eta_paged_decode(
+    const eta_dims_t* dims, int32_t n_pages, const eta_bf16_t* q, const float* tau,
+    const eta_bf16_t* K_pool, const eta_bf16_t* V_pool, const int32_t* table,
+    const int32_t* lengths, const int32_t* union_idx, const int32_t* union_cnt, float T,
+    float scale, eta_prune_t prune, const float* vsum, const int32_t* cnt,
+    eta_out_format_t o_format, void* o, float* lse, void* ws, size_t ws_bytes,
+    int32_t* dev_status, void* stream) {
+  eta_status_t st = check_pool(dims, n_pages);
+  if (st != ETA_OK) return st;
+  if (!q || !K_pool || !V_pool || !table || !lengths || !o || !lse) return ETA_ERR_INVALID_ARG;
+  if (!aligned16(K_pool) || !aligned16(V_pool) || !aligned16(q)) return ETA_ERR_INVALID_ARG;
+  if (o_format != ETA_OUT_F32 && o_format != ETA_OUT_BF16) return ETA_ERR_INVALID_ARG;
+  if (prune != ETA_PRUNE_SKIP && prune != ETA_PRUNE_FLOOR) return ETA_ERR_INVALID_ARG;
+  if (union_idx && !union_cnt) return ETA_ERR_INVALID_ARG;
+  if (prune == ETA_PRUNE_FLOOR && (!union_idx || !vsum || !cnt)) return ETA_ERR_INVALID_ARG;
+  if (tau && (!(T >= 0.f) || isinf(T))) return ETA_ERR_INVALID_ARG;
+  const int P = decode_grid();
+  const WsLayout L = ws_layout(dims, P);
+  if (!ws || ws_bytes < L.total || !aligned16(ws)) return ETA_ERR_WORKSPACE;
+  if (scale == 0.f) scale = 1.f / sqrtf((float)dims->d);
+  char* w = static_cast<char*>(ws);
+  int32_t* plan = reinterpret_cast<int32_t*>(w + L.plan);
+  int32_t* row_off = reinterpret_cast<int32_t*>(w + L.row_off);
+  int32_t* cta_row = reinterpret_cast<int32_t*>(w + L.cta_row);
+  float* part_ml = reinterpret_cast<float*>(w + L.part_ml);
+  float* part_o = reinterpret_cast<float*>(w + L.part_o);
+  const int R = dims->B * dims->Hkv, NB = num_blocks(dims);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+
+  CUtensorMap mk, mv, mq;
+  const uint64_t kv_rows = (uint64_t)n_pages * dims->Hkv * dims->blk;
+  if (!make_map(&mk, K_pool, kv_rows, 64, dims->d) ||
+      !make_map(&mv, V_pool, kv_rows, 64, dims->d) ||
+      !make_map(&mq, q, (uint64_t)dims->B * dims->Hq, 16, dims->d))
+    return ETA_ERR_CUDA;
+  st = union_idx ? launch_k(plan_kernel<false>, dim3(1), dim3(kPlanThreads), 0, s, R, dims->Hkv,
+                            NB, dims->blk, dims->T_max, union_cnt, lengths, P, row_off, cta_row,
+                            plan, dev_status)
+                 : launch_k(plan_kernel<true>, dim3(1), dim3(kPlanThreads), 0, s, R, dims->Hkv,
+                            NB, dims->blk, dims->T_max, union_cnt, lengths, P, row_off, cta_row,
+                            plan, dev_status);
+  if (st != ETA_OK) return st;
+
+  tc::TcParams prm = {};
+  prm.Hq = dims->Hq; prm.Hkv = dims->Hkv; prm.T_max = dims->T_max; prm.NB = NB;
+  prm.blk = dims->blk; prm.scale = scale; prm.invT = T == 0.f ? -1.f : 1.f / T; prm.tau = tau;
+  prm.lengths = lengths; prm.union_idx = union_idx; prm.row_off = row_off;
+  prm.cta_row = cta_row; prm.plan = plan; prm.part_o = part_o; prm.part_ml = part_ml;
+  prm.status = dev_status; prm.R = R; prm.counts = union_cnt; prm.row_off_g = row_off;
+  prm.plan_g = plan; prm.table = table; prm.n_pages = n_pages;
+  // an fp32 output takes P in three terms, so that the product with V is as exact as
+  // fp32 sums; a bf16 output's own rounding is far above the two-term split's 2^-16
+  const bool wide = o_format == ETA_OUT_F32, d64 = dims->d == 64, gate = tau != nullptr;
+  switch (dims->Hq / dims->Hkv) {
+    case 1: st = launch_paged_g<1>(gate, d64, wide, mk, mv, mq, prm, P, s); break;
+    case 2: st = launch_paged_g<2>(gate, d64, wide, mk, mv, mq, prm, P, s); break;
+    case 4: st = launch_paged_g<4>(gate, d64, wide, mk, mv, mq, prm, P, s); break;
+    default: st = launch_paged_g<8>(gate, d64, wide, mk, mv, mq, prm, P, s); break;
+  }
+  if (st != ETA_OK) return st;
+
+  CombineParams cp;
+  cp.Hq = dims->Hq; cp.Hkv = dims->Hkv; cp.NB = NB; cp.blk = dims->blk; cp.T_max = dims->T_max;
+  cp.P = P; cp.floor_mode = prune == ETA_PRUNE_FLOOR ? 1 : 0;
+  cp.row_off = row_off; cp.plan = plan; cp.union_idx = union_idx; cp.lengths = lengths;
+  cp.cnt = cnt; cp.vsum = vsum; cp.part_o = part_o; cp.part_ml = part_ml; cp.o = o; cp.lse = lse;
+  cp.status = dev_status;
+  return launch_combine(dims, cp, s, o_format == ETA_OUT_BF16);
 }
 
 // ---------------------------------------------------------------- decode without a workspace

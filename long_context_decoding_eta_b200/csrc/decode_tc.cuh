@@ -54,6 +54,7 @@ constexpr int SM_MISC = SM_P + 2 * PBUF;
 constexpr int NWARP_SM = 4;                         // softmax / correction warps
 constexpr int NT = (NWARP_SM + 2) * 32;
 constexpr int kTmemCols = 64;                       // S: 2 x 16, O: 2 x 16
+constexpr int kTmemColsWide = 128;                  // S: 2 x 16, O: 2 x 32
 
 struct TcStage {
   int row;
@@ -74,6 +75,11 @@ struct TcMisc {
   int abort_flag;
 };
 constexpr int SMEM_BYTES = SM_MISC + (int)sizeof(TcMisc) + 1024;   // + alignment slack
+// P^T of 32 columns (the three-term split of 8 heads) takes both P buffers for one, and
+// has its second one behind the misc area
+constexpr int SM_PWIDE = (SM_MISC + (int)sizeof(TcMisc) + 127) / 128 * 128;
+constexpr int SMEM_BYTES_WIDE = SM_PWIDE + 2 * PBUF + 1024;
+static_assert(SMEM_BYTES_WIDE <= 227 * 1024, "paged decode shared memory");
 
 // The fused decode step's own shared state, after the decode's barriers: the
 // screening ring's barriers and item records, and the merge scratch.
@@ -179,6 +185,9 @@ struct TcParams {
   const int32_t* counts;
   int32_t* row_off_g;
   int32_t* plan_g;
+  // paged cache: the page of block j of row b is table[b * NB + j], in [0, n_pages)
+  const int32_t* table;
+  int n_pages;
 };
 
 // In-kernel merge of the fused step: the CTA that writes the last partial slot of
@@ -263,8 +272,12 @@ ETA_DEV void plan_local(const int32_t* counts, int R, int NB, int* row_off, Fuse
 // DD (head dimension) 128, or 64: then one 64-dim box per K/V sub-tile and for the
 // query rows, QK^T in 4 steps of 16 dims, and P V still M = 128 (the V tile's upper
 // 64-dim half stays zero, so those accumulator rows are zero and not written out).
+// PAGED: K and V are page pools [n_pages, Hkv, blk, d] behind p.table, every block of a
+// row is taken when p.union_idx is NULL, and DENSE means "no gate" alone.
+// NS: the bf16 terms that P is the sum of (2: 2^-16 relative; 3: 2^-24, the rounding of fp32 itself), in NS * G
+// columns of P^T.
 template <int G, bool DENSE, bool LOCAL, bool FLAGS, bool PDL_IN = false, bool PLAN_IN = false,
-          int DD = 128>
+          int DD = 128, bool PAGED = false, int NS = 2>
 ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const CUtensorMap* tmV,
                             const CUtensorMap* tmQ, const TcParams& p, const FuseCtx& fx) {
   static_assert(G >= 1 && G <= 8, "G");
@@ -272,7 +285,14 @@ ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const C
   constexpr int NHALF = DD / 64;   // 64-dim boxes per K/V sub-tile and per query tile
   static_assert(!(LOCAL && DENSE), "the in-kernel merge is for the sparse decode");
   static_assert(!FLAGS || LOCAL, "flags come with the local plan");
-  static_assert(!PLAN_IN || (PDL_IN && !DENSE && !LOCAL), "plan in the standalone sparse decode");
+  static_assert(!PLAN_IN || (PDL_IN && (!DENSE || PAGED) && !LOCAL),
+                "plan in the standalone sparse decode");
+  static_assert(NS == 2 || (NS == 3 && PAGED && !PLAN_IN), "three terms in the paged decode");
+  constexpr int NP = NS * G <= 16 ? 16 : 32;          // columns of P^T and of O^T
+  constexpr int OFF_P1 = NP == 16 ? SM_P + PBUF : SM_PWIDE;   // the second P^T buffer
+  constexpr int TCOLS = NP == 16 ? kTmemCols : kTmemColsWide;
+  constexpr uint32_t kIdescPVn =
+      NP == 16 ? kIdescPV : (kIdescPV & ~(0x3fu << 17)) | ((32u >> 3) << 17);
   TcMisc* ms = reinterpret_cast<TcMisc*>(smem + SM_MISC);
   const int32_t* plan = p.plan;
   const int32_t* row_off = p.row_off;
@@ -295,8 +315,10 @@ ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const C
     uint4* v = reinterpret_cast<uint4*>(smem + s * STAGE_BYTES + OFF_V0);
     for (int i = threadIdx.x; i < 2 * HALF / 16; i += NT) v[i] = make_uint4(0, 0, 0, 0);
   }
-  for (int i = threadIdx.x; i < 2 * PBUF / 16; i += NT)
+  for (int i = threadIdx.x; i < 2 * PBUF / 16; i += NT) {
     reinterpret_cast<uint4*>(smem + SM_P)[i] = make_uint4(0, 0, 0, 0);
+    if constexpr (NP == 32) reinterpret_cast<uint4*>(smem + OFF_P1)[i] = make_uint4(0, 0, 0, 0);
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < NSTAGE; ++s) {
       mbar_init(&ms->full[s], 1);
@@ -317,7 +339,7 @@ ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const C
   if (warp == NWARP_SM + 1) {   // MMA warp owns the TMEM allocation
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&ms->tmem_base)),
-                 "r"(kTmemCols));
+                 "r"(TCOLS));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   tc_fence_before();
@@ -347,7 +369,7 @@ ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const C
     if (a >= Ntot) {   // uniform: no share, release TMEM (nothing was issued) and leave
       if (warp == NWARP_SM + 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                     "r"(kTmemCols));
+                     "r"(TCOLS));
       return;
     }
     e = min(a + chunk, Ntot);
@@ -364,8 +386,10 @@ ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const C
       }
       int roff = row_off[r], rend = row_off[r + 1];
       int it = 0;
-      int pend_row = -1, pend_t0 = 0, pend_nv = 0;   // a lone sub-tile waiting for a partner
-      auto emit = [&](int row, int t0a, int nva, int t0b, int nvb, int flags) -> bool {
+      // a lone sub-tile waiting for a partner: its pair, first token, TMA row, valid keys
+      int pend_row = -1, pend_t0 = 0, pend_y = 0, pend_nv = 0;
+      auto emit = [&](int row, int t0a, int ya, int nva, int t0b, int yb, int nvb,
+                      int flags) -> bool {
         const int s = it % NSTAGE;
         const uint32_t ph = (uint32_t)(it / NSTAGE) & 1u;
         if (!flags && !ETA_IN_BOUNDS(row, p.R, p.status)) return false;
@@ -383,7 +407,7 @@ ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const C
           tma_load_2d(st + OFF_Q0, tmQ, 0, qrow, &ms->full[s]);
           if constexpr (NHALF == 2) tma_load_2d(st + OFF_Q1, tmQ, 64, qrow, &ms->full[s]);
           for (int u = 0; u < nsub; ++u) {
-            const int y = row * p.T_max + (u == 0 ? t0a : t0b);
+            const int y = u == 0 ? ya : yb;
             tma_load_2d(st + OFF_K0 + u * SUB_HALF, tmK, 0, y, &ms->full[s]);
             tma_load_2d(st + OFF_V0 + u * SUB_HALF, tmV, 0, y, &ms->full[s]);
             if constexpr (NHALF == 2) {
@@ -426,7 +450,7 @@ ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const C
           ro = re;
           re = row_off[rr + 1];
         }
-        if (DENSE) return pos - ro;
+        if (PAGED ? p.union_idx == nullptr : DENSE) return pos - ro;
         if (!row_ready(rr) || !ETA_IN_BOUNDS(pos - ro, p.NB, p.status)) {
           rows_ok = false;
           return 0;
@@ -435,37 +459,59 @@ ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const C
       };
       int nr = r, nroff = roff, nrend = rend;
       int j_next = a < e ? fetch(a, nr, nroff, nrend) : 0;
+      // paged: the page of position pos+1 is looked up with its block index, one
+      // position ahead, and the block index of pos+2 before that
+      auto page_of = [&](int rr, int j) -> int {
+        return (j >= 0 && j < p.NB) ? p.table[(size_t)(rr / p.Hkv) * p.NB + j] : -1;
+      };
+      int r2 = nr, roff2 = nroff, rend2 = nrend, j_next2 = 0, page_next = -1;
+      if constexpr (PAGED) {
+        if (a < e) {
+          page_next = page_of(nr, j_next);
+          if (a + 1 < e) j_next2 = fetch(a + 1, r2, roff2, rend2);
+        }
+      }
       for (int pos = a; pos < e && ok; ++pos) {
         if (!rows_ok) {
           ok = false;
           break;
         }
-        const int j = j_next;
+        const int j = j_next, page = page_next;
         r = nr; roff = nroff; rend = nrend;
-        if (pos + 1 < e) j_next = fetch(pos + 1, nr, nroff, nrend);
+        if constexpr (PAGED) {
+          j_next = j_next2;
+          nr = r2; nroff = roff2; nrend = rend2;
+          if (pos + 1 < e) page_next = page_of(nr, j_next);
+          if (pos + 2 < e) j_next2 = fetch(pos + 2, r2, roff2, rend2);
+        } else {
+          if (pos + 1 < e) j_next = fetch(pos + 1, nr, nroff, nrend);
+        }
         const int b = r / p.Hkv;
         const int len = min(max(p.lengths[b], 0), p.T_max);
-        if (j < 0 || j >= p.NB || j * p.blk >= len) {
+        if (j < 0 || j >= p.NB || j * p.blk >= len ||
+            (PAGED && (page < 0 || page >= p.n_pages))) {
           set_status(p.status, ETA_DEVSTAT_BAD_BLOCK);
           continue;
         }
+        const int y0 = PAGED ? (page * p.Hkv + r % p.Hkv) * p.blk : r * p.T_max + j * p.blk;
         for (int sub = 0; sub < p.blk / kSubKeys && ok; ++sub) {
           const int t0 = j * p.blk + sub * kSubKeys;
+          const int y = y0 + sub * kSubKeys;
           const int nv = min(kSubKeys, len - t0);
           if (nv <= 0) break;
           if (pend_row < 0) {
-            pend_row = r; pend_t0 = t0; pend_nv = nv;
+            pend_row = r; pend_t0 = t0; pend_y = y; pend_nv = nv;
           } else if (pend_row == r) {
-            ok = emit(r, pend_t0, pend_nv, t0, nv, 0);
+            ok = emit(r, pend_t0, pend_y, pend_nv, t0, y, nv, 0);
             pend_row = -1;
           } else {
-            ok = emit(pend_row, pend_t0, pend_nv, 0, 0, 0);
-            pend_row = r; pend_t0 = t0; pend_nv = nv;
+            ok = emit(pend_row, pend_t0, pend_y, pend_nv, 0, 0, 0, 0);
+            pend_row = r; pend_t0 = t0; pend_y = y; pend_nv = nv;
           }
         }
       }
-      if (ok && pend_row >= 0) ok = emit(pend_row, pend_t0, pend_nv, 0, 0, 0);
-      if (ok) ok = emit(-1, 0, 0, 0, 0, 1);
+      if (ok && pend_row >= 0) ok = emit(pend_row, pend_t0, pend_y, pend_nv, 0, 0, 0, 0);
+      if (ok) ok = emit(-1, 0, 0, 0, 0, 0, 0, 1);
       if (!ok) {
         set_status(p.status, ETA_DEVSTAT_TIMEOUT);
         *abort_flag = 1;
@@ -485,12 +531,12 @@ ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const C
         if (!mbar_wait(&ms->o_free[pb], ph ^ 1u, abort_flag)) return false;
         tc_fence_after();
         const uint32_t v0 = smem_u32(smem + s * STAGE_BYTES + OFF_V0);
-        const uint32_t pbase = smem_u32(smem + SM_P + pb * PBUF);
+        const uint32_t pbase = smem_u32(smem + (pb ? OFF_P1 : SM_P));
 #pragma unroll
         for (int kk = 0; kk < kTileKeys / 16; ++kk) {
           const uint64_t da = smem_desc(v0 + kk * 2048, HALF, 1024, kSwizzle128);
           const uint64_t db = smem_desc(pbase + kk * 256, 128, 16 * 128, kSwizzleNone);
-          mma_f16(tO0 + pb * 16, da, db, kIdescPV, kk > 0 ? 1u : 0u);
+          mma_f16(tO0 + pb * NP, da, db, kIdescPVn, kk > 0 ? 1u : 0u);
         }
         mma_commit(&ms->o_full[pb]);
         mma_commit(&ms->empty[s]);
@@ -546,13 +592,23 @@ ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const C
       const int pb = k & 1;
       if (!wwait(&ms->o_full[pb], (uint32_t)(k >> 1) & 1u)) return false;
       tc_fence_after();
-      float c[16];
-      tmem_ld16(tO0 + pb * 16 + lane_sel, c);
+      float c[NP];
+      {
+        float (&c0)[16] = reinterpret_cast<float (&)[16]>(c[0]);
+        tmem_ld16(tO0 + pb * NP + lane_sel, c0);
+        if constexpr (NP == 32) {
+          float (&c1)[16] = reinterpret_cast<float (&)[16]>(c[16]);
+          tmem_ld16(tO0 + pb * NP + 16 + lane_sel, c1);
+        }
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms->o_free[pb]);
 #pragma unroll
-      for (int h = 0; h < G; ++h) o_acc[h] = fmaf(o_acc[h], alpha_prev[h], c[h] + c[G + h]);
+      for (int h = 0; h < G; ++h) {
+        const float lo = NS == 3 ? c[G + h] + c[2 * G + h] : c[G + h];
+        o_acc[h] = fmaf(o_acc[h], alpha_prev[h], c[h] + lo);
+      }
       return true;
     };
     auto flush = [&](int row) {
@@ -688,7 +744,7 @@ ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const C
       }
       named_bar_sync(1, NWARP_SM * 32);
       float alpha[G];
-      uint32_t pk0[4] = {0, 0, 0, 0}, pk1[4] = {0, 0, 0, 0};   // P^T columns 0-7, 8-15
+      uint32_t pk[NP / 8][4] = {};                    // P^T columns, 8 a group
 #pragma unroll
       for (int h = 0; h < G; ++h) {
         float tm = ms->red[sb][0][h];
@@ -699,23 +755,25 @@ ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const C
         const float pr = valid ? __expf(sp[h] - mnew) : 0.f;
         l_part[h] = fmaf(l_part[h], alpha[h], pr);
         m_run[h] = mnew;
-        const __nv_bfloat16 hb = __float2bfloat16_rn(pr);
-        const __nv_bfloat16 lb = __float2bfloat16_rn(pr - __bfloat162float(hb));
-        const uint32_t hu = (uint32_t)__bfloat16_as_ushort(hb);
-        const uint32_t lu = (uint32_t)__bfloat16_as_ushort(lb);
-        // column c of P^T: c = h (hi) and c = G + h (lo)
-        const int ch = h, cl = G + h;
-        if (ch < 8) pk0[ch >> 1] |= hu << ((ch & 1) * 16); else pk1[(ch - 8) >> 1] |= hu << ((ch & 1) * 16);
-        if (cl < 8) pk0[cl >> 1] |= lu << ((cl & 1) * 16); else pk1[(cl - 8) >> 1] |= lu << ((cl & 1) * 16);
+        // column k * G + h of P^T: term k of head h, each the rounding of what the terms
+        // before it leave
+        float rest = pr;
+#pragma unroll
+        for (int k = 0; k < NS; ++k) {
+          const __nv_bfloat16 tb = __float2bfloat16_rn(rest);
+          rest -= __bfloat162float(tb);
+          const int c = k * G + h;
+          pk[c >> 3][(c & 7) >> 1] |= (uint32_t)__bfloat16_as_ushort(tb) << ((c & 1) * 16);
+        }
       }
       // P^T, MN-major, no swizzle: column group cg (8 columns) at cg * 2048 B, key group
       // t / 8 at 128 B, key t % 8 at 16 B
-      unsigned char* pbuf = smem + SM_P + sb * PBUF;
-      *reinterpret_cast<uint4*>(pbuf + (t >> 3) * 128 + (t & 7) * 16) =
-          make_uint4(pk0[0], pk0[1], pk0[2], pk0[3]);
-      if (2 * G > 8)
-        *reinterpret_cast<uint4*>(pbuf + 2048 + (t >> 3) * 128 + (t & 7) * 16) =
-            make_uint4(pk1[0], pk1[1], pk1[2], pk1[3]);
+      unsigned char* pbuf = smem + (sb ? OFF_P1 : SM_P);
+#pragma unroll
+      for (int cg = 0; cg < NP / 8; ++cg)
+        if (NS * G > cg * 8)
+          *reinterpret_cast<uint4*>(pbuf + cg * 2048 + (t >> 3) * 128 + (t & 7) * 16) =
+              make_uint4(pk[cg][0], pk[cg][1], pk[cg][2], pk[cg][3]);
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms->p_full[sb]);
@@ -738,7 +796,7 @@ ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const C
   __syncthreads();
   if (warp == NWARP_SM + 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TCOLS));
   }
 }
 
@@ -751,6 +809,18 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   decode_tc_body<G, DENSE, false, false, true, PLAN_IN, DD>(smem, &tmK, &tmV, &tmQ, p,
                                                              FuseCtx{});
+}
+
+// The decode of a paged cache (GATE: thresholds given).  NS: see decode_tc_body.
+template <int G, bool GATE, int DD, int NS>
+__global__ void __launch_bounds__(NT, 1)
+decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                    const __grid_constant__ CUtensorMap tmQ, const TcParams p) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  decode_tc_body<G, !GATE, false, false, true, false, DD, true, NS>(smem, &tmK, &tmV, &tmQ, p,
+                                                                    FuseCtx{});
 }
 
 }  // namespace tc

@@ -11,6 +11,7 @@
 #include "eta_common.cuh"
 #include "eta_host.h"
 #include "meta_dev.cuh"
+#include "paged_host.h"
 
 namespace eta {
 
@@ -20,7 +21,8 @@ meta_build_kernel(int Hkv, int T_max, int blk, int NB, const eta_bf16_t* __restr
                   const eta_bf16_t* __restrict__ V, const int32_t* __restrict__ lengths,
                   int blk_begin, int nblk, void* __restrict__ cent,
                   float* __restrict__ rmax, float* __restrict__ var, int32_t* __restrict__ cnt,
-                  float* __restrict__ vsum, float* __restrict__ vardim, int32_t* status) {
+                  float* __restrict__ vsum, float* __restrict__ vardim, int32_t* status,
+                  const int32_t* __restrict__ table, int n_pages) {
   ETA_PDL_ENTRY();
   constexpr int DPL = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -34,12 +36,20 @@ meta_build_kernel(int Hkv, int T_max, int blk, int NB, const eta_bf16_t* __restr
   const int jj = blockIdx.x * kMetaWarps + warp;
   if (jj >= nblk) return;
   const int j = blk_begin + jj;
-  const int n = min(max(len - j * blk, 0), blk);
+  int n = min(max(len - j * blk, 0), blk);
   // the block's metadata slot and the tokens its keys come from
   if (!ETA_IN_BOUNDS(j, NB, status) || !ETA_RANGE_IN_BOUNDS(j * blk, j * blk + n, T_max, status))
     return;
   const size_t rowj = (size_t)r * NB + j;
-  const eta_bf16_t* kb = K + ((size_t)r * T_max + (size_t)j * blk) * D + lane * DPL;
+  long long tok0 = 0;
+  if (n > 0) {
+    tok0 = block_tokens(table, n_pages, r, Hkv, T_max, blk, NB, j, status);
+    if (tok0 < 0) {                         // a page out of range: an empty block
+      n = 0;
+      tok0 = 0;
+    }
+  }
+  const eta_bf16_t* kb = K + (size_t)tok0 * D + lane * DPL;
 
   // The keys are summed in kMetaWarps consecutive chunks of ceil(blk / kMetaWarps)
   // keys, each chunk sequentially from zero, and the chunk sums in order: exactly
@@ -120,7 +130,7 @@ meta_build_kernel(int Hkv, int T_max, int blk, int NB, const eta_bf16_t* __restr
     cnt[rowj] = n;
   }
   if (vsum) {
-    const eta_bf16_t* vb = V + ((size_t)r * T_max + (size_t)j * blk) * D + lane * DPL;
+    const eta_bf16_t* vb = V + (size_t)tok0 * D + lane * DPL;
     float a[DPL];
 #pragma unroll
     for (int i = 0; i < DPL; ++i) a[i] = 0.f;
@@ -153,41 +163,40 @@ __global__ void __launch_bounds__(kMetaWarps * 32)
 meta_tail_kernel(int Hkv, int T_max, int blk, int NB, const eta_bf16_t* __restrict__ K,
                  const eta_bf16_t* __restrict__ V, const int32_t* __restrict__ lengths,
                  void* __restrict__ cent, float* __restrict__ rmax, float* __restrict__ var,
-                 int32_t* __restrict__ cnt, float* __restrict__ vsum, float* __restrict__ vardim) {
+                 int32_t* __restrict__ cnt, float* __restrict__ vsum, float* __restrict__ vardim,
+                 int32_t* status, const int32_t* __restrict__ table, int n_pages) {
   ETA_PDL_ENTRY();
   __shared__ TailScratch<D, CF> sc;
   meta_tail_block<D, CF, kMetaWarps>(blockIdx.x, Hkv, T_max, blk, NB, K, V, lengths, cent, rmax,
-                                     var, cnt, vsum, vardim, nullptr, sc, threadIdx.x >> 5,
-                                     [] { __syncthreads(); });
+                                     var, cnt, vsum, vardim, status, sc, threadIdx.x >> 5,
+                                     [] { __syncthreads(); }, table, n_pages);
 }
 
 template <int D, int CF>
 static eta_status_t launch_meta(bool tail, const eta_dims_t* dims, int NB, int R, int blk_begin,
                                 int nblk, const eta_bf16_t* K, const eta_bf16_t* V,
                                 const int32_t* lengths, void* cent, float* rmax, float* var,
-                                int32_t* cnt, float* vsum, float* vardim, cudaStream_t s) {
+                                int32_t* cnt, float* vsum, float* vardim, cudaStream_t s,
+                                const int32_t* table, int n_pages, int32_t* status) {
   if (tail)
     return launch_k(meta_tail_kernel<D, CF>, dim3(R), dim3(kMetaWarps * 32), 0, s, dims->Hkv,
                     dims->T_max, dims->blk, NB, K, V, lengths, cent, rmax, var, cnt, vsum,
-                    vardim);
+                    vardim, status, table, n_pages);
   dim3 grid((nblk + kMetaWarps - 1) / kMetaWarps, R);
   return launch_k(meta_build_kernel<D, CF>, grid, dim3(kMetaWarps * 32), 0, s, dims->Hkv,
                   dims->T_max, dims->blk, NB, K, V, lengths, blk_begin, nblk, cent, rmax, var,
-                  cnt, vsum, vardim, (int32_t*)nullptr);
+                  cnt, vsum, vardim, status, table, n_pages);
 }
 
 }  // namespace eta
 
 using namespace eta;
 
-extern "C" eta_status_t eta_build_block_meta(const eta_dims_t* dims, const eta_bf16_t* K,
-                                             const eta_bf16_t* V, const int32_t* lengths,
-                                             int32_t blk_begin, int32_t blk_end,
-                                             eta_cent_format_t cent_format, void* cent,
-                                             float* rmax, float* var, int32_t* cnt, float* vsum,
-                                             float* vardim, void* stream) {
-  eta_status_t st = check_dims(dims);
-  if (st != ETA_OK) return st;
+static eta_status_t run_meta(const eta_dims_t* dims, const eta_bf16_t* K, const eta_bf16_t* V,
+                             const int32_t* lengths, int32_t blk_begin, int32_t blk_end,
+                             eta_cent_format_t cent_format, void* cent, float* rmax, float* var,
+                             int32_t* cnt, float* vsum, float* vardim, void* stream,
+                             const int32_t* table, int n_pages, int32_t* status) {
   if (!K || !lengths || !cent || !rmax || !var || !cnt) return ETA_ERR_INVALID_ARG;
   if (cent_format != ETA_CENT_F32 && cent_format != ETA_CENT_BF16) return ETA_ERR_INVALID_ARG;
   if (vsum && !V) return ETA_ERR_INVALID_ARG;
@@ -206,11 +215,35 @@ extern "C" eta_status_t eta_build_block_meta(const eta_dims_t* dims, const eta_b
   const bool bf = cent_format == ETA_CENT_BF16;
   if (dims->d == 128)
     return bf ? launch_meta<128, 1>(tail, dims, NB, R, blk_begin, nblk, K, V, lengths, cent, rmax,
-                                   var, cnt, vsum, vardim, s)
+                                   var, cnt, vsum, vardim, s, table, n_pages, status)
               : launch_meta<128, 0>(tail, dims, NB, R, blk_begin, nblk, K, V, lengths, cent, rmax,
-                                   var, cnt, vsum, vardim, s);
+                                   var, cnt, vsum, vardim, s, table, n_pages, status);
   return bf ? launch_meta<64, 1>(tail, dims, NB, R, blk_begin, nblk, K, V, lengths, cent, rmax,
-                                var, cnt, vsum, vardim, s)
+                                var, cnt, vsum, vardim, s, table, n_pages, status)
             : launch_meta<64, 0>(tail, dims, NB, R, blk_begin, nblk, K, V, lengths, cent, rmax,
-                                var, cnt, vsum, vardim, s);
+                                var, cnt, vsum, vardim, s, table, n_pages, status);
+}
+
+extern "C" eta_status_t eta_build_block_meta(const eta_dims_t* dims, const eta_bf16_t* K,
+                                             const eta_bf16_t* V, const int32_t* lengths,
+                                             int32_t blk_begin, int32_t blk_end,
+                                             eta_cent_format_t cent_format, void* cent,
+                                             float* rmax, float* var, int32_t* cnt, float* vsum,
+                                             float* vardim, void* stream) {
+  const eta_status_t st = check_dims(dims);
+  if (st != ETA_OK) return st;
+  return run_meta(dims, K, V, lengths, blk_begin, blk_end, cent_format, cent, rmax, var, cnt,
+                  vsum, vardim, stream, nullptr, 0, nullptr);
+}
+
+extern "C" eta_status_t eta_paged_build_block_meta(
+    const eta_dims_t* dims, int32_t n_pages, const eta_bf16_t* K_pool, const eta_bf16_t* V_pool,
+    const int32_t* table, const int32_t* lengths, int32_t blk_begin, int32_t blk_end,
+    eta_cent_format_t cent_format, void* cent, float* rmax, float* var, int32_t* cnt,
+    float* vsum, float* vardim, int32_t* dev_status, void* stream) {
+  const eta_status_t st = check_pool(dims, n_pages);
+  if (st != ETA_OK) return st;
+  if (!table) return ETA_ERR_INVALID_ARG;
+  return run_meta(dims, K_pool, V_pool, lengths, blk_begin, blk_end, cent_format, cent, rmax,
+                  var, cnt, vsum, vardim, stream, table, n_pages, dev_status);
 }

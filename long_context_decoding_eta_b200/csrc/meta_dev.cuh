@@ -43,6 +43,20 @@ ETA_DEV void store_centroid(void* cent, size_t idx, float c) {
     reinterpret_cast<float*>(cent)[idx] = c;
 }
 
+// First token (in units of d elements) of block j of (row, KV head) r: in the row's own
+// [T_max, d] array, or, with a page table, in page table[row, j] of a pool
+// [n_pages, Hkv, blk, d]; -1 for a page out of range (BAD_BLOCK is latched).
+ETA_DEV long long block_tokens(const int32_t* table, int n_pages, int r, int Hkv, int T_max,
+                               int blk, int NB, int j, int32_t* status) {
+  if (!table) return (long long)r * T_max + (long long)j * blk;
+  const int page = table[(size_t)(r / Hkv) * NB + j];
+  if (page < 0 || page >= n_pages) {
+    set_status(status, ETA_DEVSTAT_BAD_BLOCK);
+    return -1;
+  }
+  return ((long long)page * Hkv + r % Hkv) * blk;
+}
+
 // Tail-block refresh of one (row, KV head) r after a token was appended: the same
 // arithmetic as meta_build_kernel (sequential sums over the keys in token order,
 // one division, butterfly distance sums), with the block's keys split into
@@ -67,7 +81,8 @@ ETA_DEV void meta_tail_block(int r, int Hkv, int T_max, int blk, int NB,
                              float* __restrict__ rmax, float* __restrict__ var,
                              int32_t* __restrict__ cnt, float* __restrict__ vsum,
                              float* __restrict__ vardim, int32_t* status,
-                             TailScratch<D, CF>& sc, int wid, Sync sync) {
+                             TailScratch<D, CF>& sc, int wid, Sync sync,
+                             const int32_t* __restrict__ table = nullptr, int n_pages = 0) {
   constexpr int DPL = D / 32;
   using Acc = typename TailScratch<D, CF>::Acc;
   const int warp = wid, lane = threadIdx.x & 31;
@@ -81,7 +96,25 @@ ETA_DEV void meta_tail_block(int r, int Hkv, int T_max, int blk, int NB,
     return;
   const int per = (blk + kMetaWarps - 1) / kMetaWarps;
   const size_t rowj = (size_t)r * NB + j;
-  const eta_bf16_t* kb = K + ((size_t)r * T_max + (size_t)j * blk) * D + lane * DPL;
+  const long long tok0 = block_tokens(table, n_pages, r, Hkv, T_max, blk, NB, j, status);
+  if (tok0 < 0) {                            // a page out of range: an empty block
+    if (warp == 0) {
+#pragma unroll
+      for (int i = 0; i < DPL; ++i) {
+        const size_t dj = ((size_t)r * D + lane * DPL + i) * NB + j;
+        store_centroid<CF>(cent, dj, 0.f);
+        if (vardim) vardim[dj] = 0.f;
+        if (vsum) vsum[rowj * D + lane * DPL + i] = 0.f;
+      }
+      if (lane == 0) {
+        rmax[rowj] = 0.f;
+        var[rowj] = 0.f;
+        cnt[rowj] = 0;
+      }
+    }
+    return;
+  }
+  const eta_bf16_t* kb = K + (size_t)tok0 * D + lane * DPL;
 
   // pass 1: centroid (fp32 sums, or exact fp64 sums for bf16 storage)
   for (int vw = warp; vw < kMetaWarps; vw += NWARP) {
@@ -165,7 +198,7 @@ ETA_DEV void meta_tail_block(int r, int Hkv, int T_max, int blk, int NB,
     cnt[rowj] = n;
   }
   if (vsum) {
-    const eta_bf16_t* vb = V + ((size_t)r * T_max + (size_t)j * blk) * D + lane * DPL;
+    const eta_bf16_t* vb = V + (size_t)tok0 * D + lane * DPL;
     for (int vw = warp; vw < kMetaWarps; vw += NWARP) {
       const int t_lo = min(vw * per, n), t_hi = min(t_lo + per, n);
       float a[DPL];

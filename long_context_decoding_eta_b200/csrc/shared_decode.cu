@@ -1,0 +1,1072 @@
+// Decode attention for a batch whose rows share long prefixes, each prefix read once for
+// all of its rows (include/eta.h, eta_shared_decode).  The gate is Eq. 2-3 of the
+// evolve.pub review of arXiv 2609.20888 (Methodology Assessment), on every key.
+//
+// A softmax over disjoint key sets joins exactly: with per-set maxima m_i, sums l_i =
+// sum e^(s - m_i) and weighted sums o_i, M = max m_i gives o = sum e^(m_i - M) o_i /
+// sum e^(m_i - M) l_i.  So the queries of all rows of a group (rows x G heads of one KV
+// head) attend over the prefix together, as the M side of tensor-core tiles, every row
+// attends over its own remaining keys, and the parts are joined at the end.  The prefix
+// then costs its bytes once, and rows * G flops per byte: HBM-bound for small groups,
+// bound by the tensor cores and the exponentials from about 256 (row, head) pairs on.
+//
+// Three launches:
+//   shared_plan_kernel   (one CTA) the work list.  A unit is a 128-key tile of an item; an
+//                        item is (group, KV head, up to 256 (row, head) pairs) over the
+//                        prefix, or (row, KV head) over the row's own keys.  All units,
+//                        laid end to end, are cut into equal shares, one per SM.
+//   shared_attend_kernel one CTA per share: 320 threads, warps 0-3 / 4-7 the softmax of
+//                        streams A / B, warp 8 the TMA producer, warp 9 the MMA issuer.
+//                        S_x = Q K^T and O_x += P V with M = 128 queries, N = 128 keys;
+//                        a thread owns a query row, so no row statistic is exchanged.
+//                        Two streams keep the tensor cores busy while the other stream's
+//                        exponentials run: with more than 128 pairs A and B are two query
+//                        tiles that share every K/V tile; else they take alternate K/V
+//                        tiles of the one query tile, with accumulators of their own.
+//                        TMEM: S_A S_B O_A O_B, 128 columns each; P overwrites S.
+//   shared_combine_kernel  joins the parts of every (row, head).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "combine_dev.cuh"
+#include "decode_tc.cuh"
+#include "eta_common.cuh"
+#include "paged_host.h"
+#include "tma_host.h"
+
+namespace eta {
+namespace sd {
+
+using tc::fence_async_smem;
+using tc::mma_commit;
+using tc::mma_f16;
+using tc::smem_desc;
+using tc::tc_fence_after;
+using tc::tc_fence_before;
+using tc::tma_load_2d;
+
+constexpr int TILE = 128;                       // query rows and keys of a tile
+constexpr int SUB = 64;                         // keys of a TMA box (half a tile)
+constexpr int HALF = TILE * 128;                // [128 rows x 64 dims] bf16 = 16 KB
+constexpr int NKV = 2;                          // K/V ring stages
+constexpr int NSEG = 2;                         // segment records in flight
+constexpr int NT = 320;
+constexpr int kPlan = 1024;
+constexpr int kTmemCols = 512;
+constexpr float kRescale = 8.0f;                // rescale O when the max grows by > 8 (e^8)
+constexpr float kLog2e = 1.4426950408889634f;
+enum Gate { NONE = 0, HARD = 1, SOFT = 2 };
+
+// ------------------------------------------------------------------------- work list
+struct GroupRec {
+  int off;        // first unit
+  int nt;         // units (key tiles) of an item; 0: nothing is shared
+  int npairs;     // 256-row items per KV head
+  int row0, nrows;
+  int leader;     // the row whose table names the prefix pages
+  int nb;         // shared blocks
+  int rows;       // partial rows of a slot
+  int base;       // first partial row of the group's slots
+  int cf;         // CTA of its first unit
+};
+
+struct RowRec {
+  int off;        // first unit, after all prefix units
+  int nt;         // units per KV head
+  int start;      // first block that the row reads by itself
+  int group;      // the group it shares a prefix with, or -1
+};
+
+struct Head {
+  int prefix_units, units, share, suffix_base;
+};
+
+struct Ws {
+  Head* head;
+  GroupRec* grp;
+  RowRec* row;
+  int32_t* cta;         // per CTA: the group (or n_groups + row) of its first unit
+  float* part_ml;
+  float* part_o;
+};
+
+struct PlanParams {
+  int B, Hkv, G, NB, blk, n_groups, P;
+  const int32_t *lengths, *group_off, *prefix_len;
+  Ws ws;
+  int32_t* status;
+};
+
+template <typename T>
+ETA_DEV T cta_scan(T v, T* wsum, T& total) {    // exclusive, over kPlan threads
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  T incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) wsum[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    const T w = wsum[lane];
+    T wi = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const T y = __shfl_up_sync(0xffffffffu, wi, o);
+      if (lane >= o) wi += y;
+    }
+    wsum[lane] = wi - w;
+    if (lane == 31) wsum[32] = wi;
+  }
+  __syncthreads();
+  const T r = wsum[warp] + incl - v;
+  total = wsum[32];
+  __syncthreads();
+  return r;
+}
+
+__global__ void __launch_bounds__(kPlan) shared_plan_kernel(const PlanParams p) {
+  ETA_PDL_ENTRY();
+  __shared__ int wsum[33];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cap = p.NB * p.blk;
+  bool bad = false;
+  for (int g = threadIdx.x; g < p.n_groups; g += kPlan) {
+    const int r0 = p.group_off[g], r1 = p.group_off[g + 1];
+    bad |= r0 < 0 || r1 < r0 || r1 > p.B;
+  }
+  for (int b = threadIdx.x; b < p.B; b += kPlan) {
+    p.ws.row[b].start = 0;
+    p.ws.row[b].group = -1;
+    const int len = p.lengths[b];
+    if (len < 0 || len > cap) set_status(p.status, ETA_DEVSTAT_BAD_LENGTH);
+  }
+  bad = __syncthreads_or(bad);
+  if (bad) set_status(p.status, ETA_DEVSTAT_BAD_ROW);
+  else if (threadIdx.x == 0 && (p.group_off[0] != 0 || p.group_off[p.n_groups] != p.B))
+    set_status(p.status, ETA_DEVSTAT_BAD_ROW);
+  // a warp per group: who shares, and whose table is read
+  for (int g = warp; g < p.n_groups; g += kPlan / 32) {
+    const int r0 = bad ? 0 : p.group_off[g], r1 = bad ? 0 : p.group_off[g + 1];
+    int pre = p.prefix_len[g];
+    if (pre < 0 || pre > cap) {
+      if (lane == 0) set_status(p.status, ETA_DEVSTAT_BAD_LENGTH);
+      pre = min(max(pre, 0), cap);
+    }
+    const int nb = pre / p.blk;
+    int first = 0x7fffffff, count = 0;
+    if (nb > 0)
+      for (int r = r0 + lane; r < r1; r += 32)
+        if (min(p.lengths[r], cap) >= nb * p.blk) {
+          first = min(first, r);
+          ++count;
+        }
+    first = __reduce_min_sync(0xffffffffu, first);
+    count = __reduce_add_sync(0xffffffffu, count);
+    const bool share = count > 1;
+    if (share)
+      for (int r = r0 + lane; r < r1; r += 32)
+        if (min(p.lengths[r], cap) >= nb * p.blk) {
+          p.ws.row[r].start = nb;
+          p.ws.row[r].group = g;
+        }
+    if (lane == 0) {
+      GroupRec rec;
+      const int rows = (r1 - r0) * p.G;
+      rec.nt = share ? (nb * p.blk + TILE - 1) / TILE : 0;
+      rec.npairs = (rows + 2 * TILE - 1) / (2 * TILE);
+      rec.row0 = r0;
+      rec.nrows = r1 - r0;
+      rec.leader = first;
+      rec.nb = nb;
+      rec.rows = rec.npairs > 1 ? 2 * TILE : rows <= TILE ? 2 * rows : rows;
+      rec.off = rec.base = rec.cf = 0;
+      p.ws.grp[g] = rec;
+    }
+  }
+  __syncthreads();
+  int carry = 0, total;
+  for (int g0 = 0; g0 < p.n_groups; g0 += kPlan) {
+    const int g = g0 + threadIdx.x;
+    int n = 0;
+    if (g < p.n_groups) n = p.Hkv * p.ws.grp[g].npairs * p.ws.grp[g].nt;
+    const int off = carry + cta_scan(n, wsum, total);
+    if (g < p.n_groups) p.ws.grp[g].off = off;
+    carry += total;
+  }
+  const int prefix_units = carry;
+  for (int b0 = 0; b0 < p.B; b0 += kPlan) {
+    const int b = b0 + threadIdx.x;
+    int nt = 0;
+    if (b < p.B) {
+      const int len = min(max(p.lengths[b], 0), cap);
+      nt = (max(len - p.ws.row[b].start * p.blk, 0) + TILE - 1) / TILE;
+      p.ws.row[b].nt = nt;
+    }
+    const int off = carry + cta_scan(nt * p.Hkv, wsum, total);
+    if (b < p.B) p.ws.row[b].off = off;
+    carry += total;
+  }
+  const int units = carry;
+  const int share = max((units + p.P - 1) / p.P, 1);
+  // the item that every CTA starts in, and where a group's partial results go
+  carry = 0;
+  for (int g0 = 0; g0 < p.n_groups; g0 += kPlan) {
+    const int g = g0 + threadIdx.x;
+    int rows = 0, n = 0, off = 0, cf = 0;
+    if (g < p.n_groups) {
+      off = p.ws.grp[g].off;
+      const int items = p.Hkv * p.ws.grp[g].npairs;
+      n = items * p.ws.grp[g].nt;
+      if (n > 0) {
+        cf = off / share;
+        rows = ((off + n - 1) / share - cf + items) * p.ws.grp[g].rows;
+        for (int c = (off + share - 1) / share; c * share < off + n; ++c) p.ws.cta[c] = g;
+      }
+    }
+    const int base = carry + cta_scan(rows, wsum, total);
+    if (g < p.n_groups) {
+      p.ws.grp[g].base = base;
+      p.ws.grp[g].cf = cf;
+    }
+    carry += total;
+  }
+  for (int b = threadIdx.x; b < p.B; b += kPlan) {
+    const int off = p.ws.row[b].off, n = p.ws.row[b].nt * p.Hkv;
+    for (int c = (off + share - 1) / share; c * share < off + n; ++c) p.ws.cta[c] = p.n_groups + b;
+  }
+  if (threadIdx.x == 0) *p.ws.head = Head{prefix_units, units, share, carry};
+}
+
+// ---------------------------------------------------------------------------- attend
+struct Seg {
+  int live;             // 0: no more segments
+  int pair;             // streams are two query tiles (else alternate key tiles of one)
+  int ntiles;
+  int row0;             // batch row of query row 0 of stream A
+  int kvh;
+  int mA, mB;           // valid query rows of the streams' tiles
+  int partA, partB;     // first partial row of each stream
+  int check;            // prefix: rows that do not share it are left out
+};
+
+struct Misc {
+  uint64_t q_full, q_empty, kv_full[NKV], kv_empty[NKV];
+  uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
+  uint64_t seg_full[NSEG], seg_empty[NSEG], fin;
+  Seg seg[NSEG];
+  int2 nv[NKV];         // valid keys of the stage's two 64-key halves
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int NH = D / 64;                     // 64-dim boxes
+  static constexpr int Q_TILE = NH * HALF;              // one query tile
+  static constexpr int STAGE = 2 * NH * HALF;           // K then V
+  static constexpr int OFF_Q = 0;                       // tiles A, B
+  static constexpr int OFF_KV = 2 * Q_TILE;
+  static constexpr int OFF_MISC = OFF_KV + NKV * STAGE;
+  static constexpr int SMEM = OFF_MISC + (int)sizeof(Misc) + 1024;
+};
+static_assert(Cfg<128>::SMEM <= 227 * 1024, "shared decode shared memory");
+
+struct AttendParams {
+  int B, Hq, Hkv, G, NB, blk, n_pages, n_groups;
+  float scale, invT;
+  const float* tau;
+  const int32_t *table, *lengths;
+  Ws ws;
+  int part_rows;        // partial rows of the workspace (the checked build's limit)
+  int32_t* status;
+};
+
+// kind::f16, D fp32, A/B bf16, M = 128
+template <int N>
+constexpr uint32_t idesc() {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+ETA_DEV void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+
+ETA_DEV void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+ETA_DEV void tmem_st32(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::
+          "r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+      "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
+      "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+      "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+
+ETA_DEV void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+ETA_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+ETA_DEV float ex2_approx(float x) {             // 2^x on the SFU; -inf gives 0
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+ETA_DEV float tanh_approx(float x) {
+  float y;
+  asm("tanh.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+ETA_DEV float fmax3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Box of 64 dims x G heads x `rows` batch rows of q [B, Hq, d]: the query rows packed as
+// (row, head), 128 bytes each.
+ETA_DEV void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Jobs of a segment, in the order the MMA warp takes them: job n belongs to stream n & 1;
+// pair: both streams take every key tile; else stream x takes the tiles of its parity.
+ETA_DEV int jobs_of(const Seg& s, int x) {
+  return s.pair ? s.ntiles : (s.ntiles + 1 - x) >> 1;
+}
+
+// GATE: Gate.  NS: the bf16 terms of P (1: bf16 output, 2: fp32 output).
+template <int D, int GATE, int NS>
+__global__ void __launch_bounds__(NT, 1)
+shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
+                     const __grid_constant__ CUtensorMap tmQ1,
+                     const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const AttendParams p) {
+  using C = Cfg<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Misc* ms = reinterpret_cast<Misc*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = &ms->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&ms->q_full, 1);
+    mbar_init(&ms->q_empty, 1);
+    for (int s = 0; s < NKV; ++s) {
+      mbar_init(&ms->kv_full[s], 1);
+      mbar_init(&ms->kv_empty[s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&ms->s_full[x], 1);
+      mbar_init(&ms->p_full[x], 4);
+      mbar_init(&ms->pv_done[x], 1);
+      mbar_init(&ms->o_free[x], 4);
+    }
+    for (int s = 0; s < NSEG; ++s) {
+      mbar_init(&ms->seg_full[s], 1);
+      mbar_init(&ms->seg_empty[s], 9);          // 8 softmax warps and the MMA warp
+    }
+    mbar_init(&ms->fin, 1);
+    ms->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&ms->tmem_base)),
+                 "r"(kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms->tmem_base;
+  const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 384};
+  ETA_PDL_ENTRY();
+
+  if (warp == 8) {
+    // ------------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      const Head hd = *p.ws.head;
+      const int a = blockIdx.x * hd.share, e = min(a + hd.share, hd.units);
+      bool ok = true;
+      int nseg = 0, nst = 0;                     // segments, stages issued so far
+      int at = a < e ? p.ws.cta[blockIdx.x] : 0;
+      int pos = a;
+      while (ok) {
+        Seg s = {};
+        int key0 = 0, key_end = 0, trow = 0, mrows = 0;
+        while (pos < e && pos < hd.prefix_units) {
+          const GroupRec g = p.ws.grp[at];
+          const int items = p.Hkv * g.npairs, local = pos - g.off;
+          if (g.nt == 0 || local >= items * g.nt) {
+            if (++at >= p.n_groups) break;       // cannot happen: a unit has an item
+            continue;
+          }
+          const int item = local / g.nt, t = local - item * g.nt;
+          const int pair = item % g.npairs, i0 = pair * 2 * TILE;
+          const int left = g.nrows * p.G - i0;
+          s.live = 1;
+          s.pair = left > TILE;
+          s.ntiles = min(g.nt - t, e - pos);
+          s.row0 = g.row0 + i0 / p.G;
+          s.kvh = item / g.npairs;
+          s.mA = min(left, TILE);
+          s.mB = s.pair ? min(left - TILE, TILE) : s.mA;
+          s.partA = g.base + ((int)blockIdx.x - g.cf + item) * g.rows;
+          s.partB = s.partA + (!s.pair && g.npairs == 1 ? s.mA : TILE);
+          s.check = 1;
+          key0 = t * TILE;
+          key_end = g.nb * p.blk;
+          trow = g.leader;
+          mrows = TILE;
+          break;
+        }
+        if (!s.live && pos < e) {
+          int b = at - p.n_groups;
+          if (b < 0) {
+            b = 0;
+            at = p.n_groups;
+          }
+          while (b < p.B && pos >= p.ws.row[b].off + p.ws.row[b].nt * p.Hkv) ++b;
+          at = p.n_groups + b;
+          if (b < p.B) {
+            const RowRec r = p.ws.row[b];
+            const int local = pos - r.off, g = local / r.nt, t = local - g * r.nt;
+            s.live = 1;
+            s.pair = 0;
+            s.ntiles = min(r.nt - t, e - pos);
+            s.row0 = b;
+            s.kvh = g;
+            s.mA = s.mB = p.G;
+            s.partA = hd.suffix_base + ((int)blockIdx.x + b * p.Hkv + g) * 2 * p.G;
+            s.partB = s.partA + p.G;
+            key0 = r.start * p.blk + t * TILE;
+            key_end = min(max(p.lengths[b], 0), p.NB * p.blk);
+            trow = b;
+            mrows = p.G;
+          }
+        }
+        // the record, then the queries, then the tiles
+        const int sl = nseg % NSEG;
+        if (!mbar_wait(&ms->seg_empty[sl], ((uint32_t)(nseg / NSEG) & 1u) ^ 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        ms->seg[sl] = s;
+        mbar_arrive(&ms->seg_full[sl]);
+        if (!s.live) break;
+        const int* trow_p = p.table + (size_t)trow * p.NB;
+        auto page_at = [&](int key) -> int {
+          return key < key_end ? trow_p[key / p.blk] : -2;
+        };
+        int pg0 = page_at(key0), pg1 = page_at(key0 + SUB);
+        for (int t = 0; t < s.ntiles && ok; ++t, ++nst) {
+          const int st = nst % NKV, k0 = key0 + t * TILE;
+          const int c0 = pg0, c1 = pg1;
+          if (t + 1 < s.ntiles) {
+            pg0 = page_at(k0 + TILE);
+            pg1 = page_at(k0 + TILE + SUB);
+          }
+          if (!mbar_wait(&ms->kv_empty[st], ((uint32_t)(nst / NKV) & 1u) ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          int nv[2] = {max(min(key_end - k0, SUB), 0), max(min(key_end - k0 - SUB, SUB), 0)};
+          const int pg[2] = {c0, c1};
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            if (nv[u] > 0 && (pg[u] < 0 || pg[u] >= p.n_pages)) {
+              set_status(p.status, ETA_DEVSTAT_BAD_BLOCK);
+              nv[u] = 0;
+            }
+          ms->nv[st] = make_int2(nv[0], nv[1]);
+          const int nbox = (nv[0] > 0) + (nv[1] > 0);
+          mbar_arrive_expect_tx(&ms->kv_full[st], (uint32_t)(nbox * 2 * C::NH * (HALF / 2)));
+          unsigned char* kd = smem + C::OFF_KV + st * C::STAGE;
+          unsigned char* vd = kd + C::NH * HALF;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if (nv[u] == 0) continue;
+            const int key = k0 + u * SUB;
+            const int y = (pg[u] * p.Hkv + s.kvh) * p.blk + key % p.blk;
+#pragma unroll
+            for (int h = 0; h < C::NH; ++h)
+              tma_load_2d(kd + h * HALF + u * (HALF / 2), &tmK, h * 64, y, &ms->kv_full[st]);
+#pragma unroll
+            for (int h = 0; h < C::NH; ++h)
+              tma_load_2d(vd + h * HALF + u * (HALF / 2), &tmV, h * 64, y, &ms->kv_full[st]);
+          }
+          if (t == 0) {
+            // the queries of the previous segment have been read by its last Q K^T
+            if (!mbar_wait(&ms->q_empty, ((uint32_t)nseg & 1u) ^ 1u, abort_flag)) {
+              ok = false;
+              ++nst;
+              break;
+            }
+            const uint32_t bytes = (uint32_t)(mrows * 128 * C::NH) * (s.pair ? 2 : 1);
+            mbar_arrive_expect_tx(&ms->q_full, bytes);
+#pragma unroll
+            for (int h = 0; h < C::NH; ++h) {
+              unsigned char* qd = smem + C::OFF_Q + h * HALF;
+              if (s.check) {
+                tma_load_3d(qd, &tmQ, h * 64, s.kvh * p.G, s.row0, &ms->q_full);
+                if (s.pair)
+                  tma_load_3d(qd + C::Q_TILE, &tmQ, h * 64, s.kvh * p.G, s.row0 + TILE / p.G,
+                              &ms->q_full);
+              } else {
+                tma_load_3d(qd, &tmQ1, h * 64, s.kvh * p.G, s.row0, &ms->q_full);
+              }
+            }
+          }
+        }
+        pos += s.ntiles;
+        ++nseg;
+      }
+      if (!ok) {
+        // wait (bounded) for every copy this thread issued before the CTA exits
+        set_status(p.status, ETA_DEVSTAT_TIMEOUT);
+        *abort_flag = 1;
+        for (int k = max(0, nst - NKV); k < nst; ++k)
+          mbar_wait(&ms->kv_full[k % NKV], (uint32_t)(k / NKV) & 1u, nullptr);
+        if (nseg > 0) mbar_wait(&ms->q_full, (uint32_t)(nseg - 1) & 1u, nullptr);
+        mbar_wait_n(&ms->q_full, (uint32_t)nseg & 1u, nullptr, 1u << 16);
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      bool ok = true;
+      int nseg = 0, nst = 0;                     // segments done; stage of their next tile
+      int cnt[2] = {0, 0};                       // jobs done per stream
+      int used[2] = {0, 0};                      // segments in which a stream had jobs
+      const uint32_t qa[2] = {smem_u32(smem + C::OFF_Q), smem_u32(smem + C::OFF_Q + C::Q_TILE)};
+      for (;; ++nseg) {
+        const int sl = nseg % NSEG;
+        if (!mbar_wait(&ms->seg_full[sl], (uint32_t)(nseg / NSEG) & 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const Seg s = ms->seg[sl];
+        if (!s.live) break;
+        if (!mbar_wait(&ms->q_full, (uint32_t)nseg & 1u, abort_flag)) { ok = false; break; }
+        const int jobs = s.pair ? 2 * s.ntiles : s.ntiles;
+        const int base[2] = {cnt[0], cnt[1]};
+        auto tile_of = [&](int n) { return s.pair ? n >> 1 : n; };
+        auto issue_qk = [&](int n) -> bool {     // S_x = Q_x K^T
+          const int x = n & 1, k = base[x] + (n >> 1), st = (nst + tile_of(n)) % NKV;
+          const uint32_t ph = (uint32_t)((nst + tile_of(n)) / NKV) & 1u;
+          if (!mbar_wait(&ms->kv_full[st], ph, abort_flag)) return false;
+          // S_x's columns hold P_x of the stream's previous job until P V has read it
+          if (k > 0 && !mbar_wait(&ms->pv_done[x], (uint32_t)(k - 1) & 1u, abort_flag)) return false;
+          tc_fence_after();
+          const uint32_t ka = smem_u32(smem + C::OFF_KV + st * C::STAGE);
+          const uint32_t qx = qa[s.pair ? x : 0];
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (uint32_t)(kk >> 2) * HALF + (uint32_t)(kk & 3) * 32;
+            mma_f16(tS[x], smem_desc(qx + off, 16, 1024, tc::kSwizzle128),
+                    smem_desc(ka + off, 16, 1024, tc::kSwizzle128), idesc<TILE>(), kk > 0);
+          }
+          mma_commit(&ms->s_full[x]);
+          if (n == jobs - 1) mma_commit(&ms->q_empty);   // the segment's last Q K^T
+          return true;
+        };
+        auto issue_pv = [&](int n) -> bool {     // O_x += P_x V
+          const int x = n & 1, k = base[x] + (n >> 1), st = (nst + tile_of(n)) % NKV;
+          if (!mbar_wait(&ms->p_full[x], (uint32_t)k & 1u, abort_flag)) return false;
+          // a segment's first P V overwrites O_x: the last one's has to be read out
+          if (n < 2 && used[x] > 0 &&
+              !mbar_wait(&ms->o_free[x], (uint32_t)(used[x] - 1) & 1u, abort_flag))
+            return false;
+          tc_fence_after();
+          const uint32_t va = smem_u32(smem + C::OFF_KV + st * C::STAGE + C::NH * HALF);
+          constexpr uint32_t id = idesc<D>() | (1u << 16);           // V is MN-major
+#pragma unroll
+          for (int term = 0; term < NS; ++term)
+#pragma unroll
+            for (int kk = 0; kk < TILE / 16; ++kk)
+              mma_f16_ts(tO[x], tS[x] + term * 64 + kk * 8,
+                         smem_desc(va + kk * 2048, HALF, 1024, tc::kSwizzle128), id,
+                         (n >= 2 || term > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&ms->pv_done[x]);
+          if (!s.pair || x == 1) mma_commit(&ms->kv_empty[st]);
+          return true;
+        };
+        ok = issue_qk(0);
+        if (ok && jobs > 1) ok = issue_qk(1);
+        for (int n = 0; n < jobs && ok; ++n) {
+          ok = issue_pv(n);
+          if (ok && n + 2 < jobs) ok = issue_qk(n + 2);
+        }
+        if (!ok) break;
+        for (int x = 0; x < 2; ++x) {
+          const int j = jobs_of(s, x);
+          cnt[x] += j;
+          used[x] += j > 0;
+        }
+        nst += s.ntiles;
+        mbar_arrive(&ms->seg_empty[sl]);
+      }
+      if (!ok) {
+        set_status(p.status, ETA_DEVSTAT_TIMEOUT);
+        *abort_flag = 1;
+      }
+      mma_commit(&ms->fin);
+      mbar_wait(&ms->fin, 0, nullptr);
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax
+    const int x = warp >> 2;                     // stream
+    const int i = threadIdx.x & (TILE - 1);      // query row of its tile = TMEM lane
+    const uint32_t lsel = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tSx = tS[x] + lsel, tOx = tO[x] + lsel;
+    const float c1 = p.scale * kLog2e;
+    const float resc_raw = kRescale / p.scale;
+    bool ok = true;
+    int nseg = 0, nst = 0, cnt = 0;
+    auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+    };
+    for (;; ++nseg) {
+      const int sl = nseg % NSEG;
+      if (!wwait(&ms->seg_full[sl], (uint32_t)(nseg / NSEG) & 1u)) { ok = false; break; }
+      const Seg s = ms->seg[sl];
+      if (!s.live) break;
+      const int mine = x == 0 ? s.mA : s.mB;
+      const int b = s.row0 + (i + (s.pair && x ? TILE : 0)) / p.G, h = s.kvh * p.G + i % p.G;
+      const bool valid = i < mine;
+      // Gated logits in raw units u (the gated logit is scale * u), so that the scale
+      // folds into the constants: the hard gate keeps s iff s >= tau / scale; the soft
+      // gate is hs + hs * tanh(s * ta - tb), hs = s / 2, for a bf16 output (one
+      // transcendental a key, 2^-11 off, below the output's own rounding), and
+      // s / (1 + 2^(s * ta - tb)) for an fp32 one; and e^(scale * (u - m)) is
+      // 2^(u * c1 - m * c1), c1 = scale * log2(e).
+      float tau_raw = 0.f, ta = 0.f, tb = 0.f;
+      if constexpr (GATE != NONE) {
+        const float tau = valid ? p.tau[(size_t)b * p.Hq + h] : 0.f;
+        tau_raw = tau / p.scale;
+        const float f = (NS == 1 ? 0.5f : -kLog2e) * p.invT;
+        ta = p.scale * f;
+        tb = tau * f;
+      }
+      float m = -INFINITY;
+      float2 l2 = make_float2(0.f, 0.f);
+      const int jobs = jobs_of(s, x);
+      for (int j = 0; j < jobs; ++j, ++cnt) {
+        const int st = (nst + (s.pair ? j : 2 * j + x)) % NKV;
+        const uint32_t ph = (uint32_t)((nst + (s.pair ? j : 2 * j + x)) / NKV) & 1u;
+        if (!wwait(&ms->s_full[x], (uint32_t)cnt & 1u) || !wwait(&ms->kv_full[st], ph)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int2 nv = ms->nv[st];
+        float sv[TILE];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tSx + c * 32, sv + c * 32);
+        tmem_wait_ld();
+        if constexpr (GATE == HARD) {
+#pragma unroll
+          for (int c = 0; c < TILE; ++c) sv[c] = sv[c] >= tau_raw ? sv[c] : 0.f;
+        } else if constexpr (GATE == SOFT) {
+#pragma unroll
+          for (int c = 0; c < TILE; ++c) {
+            if constexpr (NS == 1) {
+              const float hs = 0.5f * sv[c];
+              sv[c] = fmaf(hs, tanh_approx(fmaf(sv[c], ta, -tb)), hs);
+            } else {
+              sv[c] = __fdividef(sv[c], 1.f + ex2_approx(fmaf(sv[c], ta, -tb)));   // 0 once 2^x is inf
+            }
+          }
+        }
+        if (nv.x < SUB || nv.y < SUB) {          // keys past the end
+#pragma unroll
+          for (int c = 0; c < TILE; ++c)
+            if ((c & (SUB - 1)) >= (c < SUB ? nv.x : nv.y)) sv[c] = -INFINITY;
+          // their V rows must be finite for P V
+          if ((i & (SUB - 1)) >= (i < SUB ? nv.x : nv.y)) {
+            unsigned char* vt = smem + C::OFF_KV + st * C::STAGE + C::NH * HALF + i * 128;
+#pragma unroll
+            for (int hh = 0; hh < C::NH; ++hh)
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                *reinterpret_cast<uint4*>(vt + hh * HALF + c * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_async_smem();
+        }
+        float pm[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) pm[u] = fmax3(sv[2 * u], sv[2 * u + 1], sv[16 + 2 * u]);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) pm[u] = fmaxf(pm[u], sv[17 + 2 * u]);
+#pragma unroll
+        for (int c = 32; c < TILE; c += 2)
+          pm[(c >> 1) & 7] = fmax3(pm[(c >> 1) & 7], sv[c], sv[c + 1]);
+        const float mx = fmaxf(fmax3(fmax3(pm[0], pm[1], pm[2]), pm[3], pm[4]),
+                               fmax3(pm[5], pm[6], pm[7]));
+        // the first tile sets the maximum; later ones rescale O (in TMEM) only when it
+        // grew by more than kRescale
+        float alpha = 1.f;
+        bool resc = false;
+        if (m == -INFINITY) {
+          m = mx;
+        } else if (mx > m + resc_raw) {
+          alpha = ex2_approx((m - mx) * c1);
+          m = mx;
+          resc = true;
+        }
+        if (__any_sync(0xffffffffu, resc)) {
+          // P V of the stream's previous job is complete: this job's Q K^T waited for it
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float ov[32];
+            tmem_ld32(tOx + c * 32, ov);
+            tmem_wait_ld();
+            uint32_t w[32];
+#pragma unroll
+            for (int u = 0; u < 32; ++u) w[u] = __float_as_uint(ov[u] * alpha);
+            tmem_st32(tOx + c * 32, w);
+          }
+          l2.x *= alpha;
+          l2.y *= alpha;
+        }
+        const float nm = m == -INFINITY ? 0.f : -m * c1;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t hi[32], lo[32];
+#pragma unroll
+          for (int u = 0; u < 32; ++u) {
+            const int k = c * 64 + 2 * u;
+            const float2 a = __ffma2_rn(make_float2(sv[k], sv[k + 1]), make_float2(c1, c1),
+                                        make_float2(nm, nm));
+            const float2 pr = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+            l2 = __fadd2_rn(l2, pr);
+            const __nv_bfloat162 hb = __floats2bfloat162_rn(pr.x, pr.y);
+            hi[u] = *reinterpret_cast<const uint32_t*>(&hb);
+            if constexpr (NS == 2) {
+              const float2 f = __bfloat1622float2(hb);
+              const __nv_bfloat162 lb = __floats2bfloat162_rn(pr.x - f.x, pr.y - f.y);
+              lo[u] = *reinterpret_cast<const uint32_t*>(&lb);
+            }
+          }
+          tmem_st32(tSx + c * 32, hi);
+          if constexpr (NS == 2) tmem_st32(tSx + 64 + c * 32, lo);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms->p_full[x]);
+      }
+      if (!ok) break;
+      nst += s.ntiles;
+      // the segment's partial result of this stream
+      if (jobs > 0) {
+        if (!wwait(&ms->pv_done[x], (uint32_t)(cnt - 1) & 1u)) { ok = false; break; }
+        tc_fence_after();
+      }
+      const bool store = valid && (!s.check || p.ws.row[b].start > 0) &&
+                         ETA_IN_BOUNDS((x ? s.partB : s.partA) + i, p.part_rows, p.status);
+      const size_t slot = (size_t)((x ? s.partB : s.partA) + i);
+      if (jobs > 0) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float ov[32];
+          tmem_ld32(tOx + c * 32, ov);
+          tmem_wait_ld();
+          if (store) {
+            float4* to = reinterpret_cast<float4*>(p.ws.part_o + slot * D + c * 32);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              to[u] = make_float4(ov[4 * u], ov[4 * u + 1], ov[4 * u + 2], ov[4 * u + 3]);
+          }
+        }
+      }
+      if (store)
+        reinterpret_cast<float2*>(p.ws.part_ml)[slot] =
+            make_float2(m * p.scale, l2.x + l2.y);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (jobs > 0) mbar_arrive(&ms->o_free[x]);
+        mbar_arrive(&ms->seg_empty[sl]);
+      }
+    }
+    if (!ok) {
+      if (lane == 0) set_status(p.status, ETA_DEVSTAT_TIMEOUT);
+      *abort_flag = 1;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(kTmemCols));
+  }
+}
+
+// --------------------------------------------------------------------------- combine
+constexpr int kCombine = 512;
+constexpr int kMaxSlots = 1024;
+
+// One CTA per (row, head): thread = (slot group, dim).  The slots are the CTAs that had a
+// piece of the row's prefix item (one or two streams each) and of its own item.
+template <int D, typename OutT>
+__global__ void __launch_bounds__(kCombine)
+shared_combine_kernel(const AttendParams p, OutT* __restrict__ o, float* __restrict__ lse) {
+  ETA_PDL_ENTRY();
+  constexpr int NG = kCombine / D;
+  __shared__ int slot[kMaxSlots];
+  __shared__ float w[kMaxSlots];
+  __shared__ float red[kCombine / 32], acc[NG][D];
+  const int b = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq, kvh = h / p.G, hg = h % p.G;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Head hd = *p.ws.head;
+  const RowRec r = p.ws.row[b];
+  int n1 = 0, first1 = 0, step1 = 0, two1 = 0, off1 = 0;    // prefix slots
+  if (r.group >= 0) {
+    const GroupRec g = p.ws.grp[r.group];
+    const int i = (b - g.row0) * p.G + hg, pair = i / (2 * TILE), ii = i % (2 * TILE);
+    const int item = kvh * g.npairs + pair, left = g.nrows * p.G - pair * 2 * TILE;
+    const int a = g.off + item * g.nt, c0 = a / hd.share;
+    n1 = (a + g.nt - 1) / hd.share - c0 + 1;
+    first1 = g.base + (c0 - g.cf + item) * g.rows + ii;
+    step1 = g.rows;
+    two1 = left <= TILE;
+    off1 = g.npairs == 1 ? left : TILE;
+  }
+  int n2 = 0, first2 = 0;                                   // the row's own slots
+  if (r.nt > 0) {
+    const int a = r.off + kvh * r.nt, c0 = a / hd.share;
+    n2 = (a + r.nt - 1) / hd.share - c0 + 1;
+    first2 = hd.suffix_base + (c0 + b * p.Hkv + kvh) * 2 * p.G + hg;
+  }
+  const int m1 = n1 * (1 + two1), n = min(m1 + 2 * n2, kMaxSlots);
+  float mx = -INFINITY;
+  for (int k = tid; k < n; k += kCombine) {
+    int s;
+    if (k < m1) s = two1 ? first1 + (k >> 1) * step1 + (k & 1) * off1 : first1 + k * step1;
+    else s = first2 + ((k - m1) >> 1) * 2 * p.G + ((k - m1) & 1) * p.G;
+    if (!ETA_IN_BOUNDS(s, p.part_rows, p.status)) s = 0;
+    slot[k] = s;
+    const float v = p.ws.part_ml[2 * (size_t)s];
+    w[k] = v;
+    mx = fmaxf(mx, v);
+  }
+  mx = warp_max(mx);
+  if (lane == 0) red[warp] = mx;
+  __syncthreads();
+  mx = red[0];
+#pragma unroll
+  for (int i = 1; i < kCombine / 32; ++i) mx = fmaxf(mx, red[i]);
+  __syncthreads();
+  float l = 0.f;
+  for (int k = tid; k < n; k += kCombine) {
+    const float e = mx == -INFINITY ? 0.f : expf(w[k] - mx);
+    w[k] = e;
+    l = fmaf(e, p.ws.part_ml[2 * (size_t)slot[k] + 1], l);
+  }
+  l = warp_sum(l);
+  if (lane == 0) red[warp] = l;
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int i = 0; i < kCombine / 32; ++i) l += red[i];
+  const int dd = tid % D, gi = tid / D;
+  float a = 0.f;
+#pragma unroll 4
+  for (int k = gi; k < n; k += NG)
+    if (w[k] > 0.f) a = fmaf(w[k], p.ws.part_o[(size_t)slot[k] * D + dd], a);
+  acc[gi][dd] = a;
+  __syncthreads();
+  if (gi == 0) {
+#pragma unroll
+    for (int i = 1; i < NG; ++i) a += acc[i][dd];
+    combine_store<D>(o, lse, (size_t)b * p.Hq + h, dd, mx, l, a);
+  }
+}
+
+// ------------------------------------------------------------------------- host side
+struct WsOff {
+  size_t head, grp, row, cta, ml, o, total;
+  int part_rows;
+};
+
+inline WsOff ws_off(const eta_dims_t* d, int n_groups, int P) {
+  // slots: at most 256 rows for every CTA and twice a group's own rows for every item,
+  // and 2 G rows for every CTA and (row, KV head)
+  const int G = d->Hq / d->Hkv;
+  WsOff w;
+  const size_t rows = (size_t)P * (2 * TILE + 2 * G) + 4 * (size_t)d->B * d->Hq;
+  size_t x = 0;
+  w.head = x; x += 256;
+  w.grp = x;  x = align_up(x + (size_t)n_groups * sizeof(GroupRec), 256);
+  w.row = x;  x = align_up(x + (size_t)d->B * sizeof(RowRec), 256);
+  w.cta = x;  x = align_up(x + (size_t)P * 4, 256);
+  w.ml = x;   x = align_up(x + rows * 8, 256);
+  w.o = x;    x = align_up(x + rows * d->d * 4, 256);
+  w.total = x;
+  w.part_rows = (int)rows;
+  return w;
+}
+
+inline int grid_size() { return std::max(sm_count(), 1); }
+
+// Sizes whose unit counts fit 32-bit sums, and whose parts fit the combine's list.
+inline eta_status_t check_sizes(const eta_dims_t* d, int32_t n_groups, int P) {
+  if (n_groups < 1 || n_groups > d->B) return ETA_ERR_INVALID_ARG;
+  const uint64_t tiles = ((uint64_t)d->T_max + TILE - 1) / TILE;
+  if (2 * tiles * d->B * d->Hkv >= (1ull << 31)) return ETA_ERR_UNSUPPORTED;
+  if ((uint64_t)P * 528 + 4ull * d->B * d->Hq >= (1ull << 31)) return ETA_ERR_UNSUPPORTED;
+  if (4 * P > kMaxSlots) return ETA_ERR_UNSUPPORTED;
+  return ETA_OK;
+}
+
+template <int D, int GATE, int NS>
+eta_status_t launch_attend(const CUtensorMap& mq, const CUtensorMap& mq1, const CUtensorMap& mk,
+                           const CUtensorMap& mv, const AttendParams& a, int P, cudaStream_t s) {
+  if (!set_smem_once<shared_attend_kernel<D, GATE, NS>>(Cfg<D>::SMEM)) return ETA_ERR_CUDA;
+  return launch_k(shared_attend_kernel<D, GATE, NS>, dim3(P), dim3(NT), Cfg<D>::SMEM, s, mq, mq1,
+                  mk, mv, a);
+}
+
+template <int D>
+eta_status_t launch_attend_d(int gate, bool two, const CUtensorMap& mq, const CUtensorMap& mq1,
+                             const CUtensorMap& mk, const CUtensorMap& mv, const AttendParams& a,
+                             int P, cudaStream_t s) {
+  switch (gate * 2 + (two ? 1 : 0)) {
+    case 0: return launch_attend<D, NONE, 1>(mq, mq1, mk, mv, a, P, s);
+    case 1: return launch_attend<D, NONE, 2>(mq, mq1, mk, mv, a, P, s);
+    case 2: return launch_attend<D, HARD, 1>(mq, mq1, mk, mv, a, P, s);
+    case 3: return launch_attend<D, HARD, 2>(mq, mq1, mk, mv, a, P, s);
+    case 4: return launch_attend<D, SOFT, 1>(mq, mq1, mk, mv, a, P, s);
+    default: return launch_attend<D, SOFT, 2>(mq, mq1, mk, mv, a, P, s);
+  }
+}
+
+// q [B, Hq, d] as (dim, head, row); box 64 x G x rows, 128-byte swizzle.
+inline bool make_map_q(CUtensorMap* m, const void* q, const eta_dims_t* d, int rows) {
+  EncodeTiledFn fn = encode_tiled();
+  if (!fn) return false;
+  cuuint64_t gdim[3] = {(cuuint64_t)d->d, (cuuint64_t)d->Hq, (cuuint64_t)d->B};
+  cuuint64_t gstride[2] = {(cuuint64_t)d->d * 2, (cuuint64_t)d->Hq * d->d * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)(d->Hq / d->Hkv), (cuuint32_t)rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), gdim, gstride, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+}  // namespace sd
+}  // namespace eta
+
+using namespace eta;
+
+extern "C" size_t eta_shared_decode_workspace_size(const eta_dims_t* dims, int32_t n_groups) {
+  if (check_dims(dims) != ETA_OK) return 0;
+  const int P = sd::grid_size();
+  if (sd::check_sizes(dims, n_groups, P) != ETA_OK) return 0;
+  return sd::ws_off(dims, n_groups, P).total;
+}
+
+extern "C" eta_status_t eta_shared_decode(const eta_dims_t* dims, int32_t n_pages,
+                                          int32_t n_groups, const eta_bf16_t* q,
+                                          const float* tau, const eta_bf16_t* K_pool,
+                                          const eta_bf16_t* V_pool, const int32_t* table,
+                                          const int32_t* lengths, const int32_t* group_off,
+                                          const int32_t* prefix_len, float T, float scale,
+                                          eta_out_format_t o_format, void* o, float* lse,
+                                          void* ws, size_t ws_bytes, int32_t* dev_status,
+                                          void* stream) {
+  eta_status_t st = check_pool(dims, n_pages);
+  if (st != ETA_OK) return st;
+  const int P = sd::grid_size();
+  if ((st = sd::check_sizes(dims, n_groups, P)) != ETA_OK) return st;
+  if (!q || !K_pool || !V_pool || !table || !lengths || !group_off || !prefix_len || !o || !lse)
+    return ETA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(K_pool) || !aligned16(V_pool) || !aligned16(o))
+    return ETA_ERR_INVALID_ARG;
+  if (o_format != ETA_OUT_F32 && o_format != ETA_OUT_BF16) return ETA_ERR_INVALID_ARG;
+  if (tau && (!(T >= 0.f) || isinf(T))) return ETA_ERR_INVALID_ARG;
+  if (!(scale >= 0.f) || isinf(scale)) return ETA_ERR_INVALID_ARG;   // the gate divides by it
+  const sd::WsOff L = sd::ws_off(dims, n_groups, P);
+  if (!ws || ws_bytes < L.total || !aligned16(ws)) return ETA_ERR_WORKSPACE;
+  if (scale == 0.f) scale = 1.f / sqrtf((float)dims->d);
+
+  const int G = dims->Hq / dims->Hkv;
+  CUtensorMap mq, mq1, mk, mv;
+  const uint64_t kv_rows = (uint64_t)n_pages * dims->Hkv * dims->blk;
+  if (!sd::make_map_q(&mq, q, dims, sd::TILE / G) || !sd::make_map_q(&mq1, q, dims, 1) ||
+      !make_map(&mk, K_pool, kv_rows, sd::SUB, dims->d) ||
+      !make_map(&mv, V_pool, kv_rows, sd::SUB, dims->d))
+    return ETA_ERR_CUDA;
+  char* w = static_cast<char*>(ws);
+  sd::Ws wp;
+  wp.head = reinterpret_cast<sd::Head*>(w + L.head);
+  wp.grp = reinterpret_cast<sd::GroupRec*>(w + L.grp);
+  wp.row = reinterpret_cast<sd::RowRec*>(w + L.row);
+  wp.cta = reinterpret_cast<int32_t*>(w + L.cta);
+  wp.part_ml = reinterpret_cast<float*>(w + L.ml);
+  wp.part_o = reinterpret_cast<float*>(w + L.o);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+
+  sd::PlanParams pp;
+  pp.B = dims->B; pp.Hkv = dims->Hkv; pp.G = G; pp.NB = num_blocks(dims); pp.blk = dims->blk;
+  pp.n_groups = n_groups; pp.P = P; pp.lengths = lengths; pp.group_off = group_off;
+  pp.prefix_len = prefix_len; pp.ws = wp; pp.status = dev_status;
+  st = launch_k(sd::shared_plan_kernel, dim3(1), dim3(sd::kPlan), 0, s, pp);
+  if (st != ETA_OK) return st;
+
+  sd::AttendParams a;
+  a.B = dims->B; a.Hq = dims->Hq; a.Hkv = dims->Hkv; a.G = G; a.NB = pp.NB; a.blk = dims->blk;
+  a.n_pages = n_pages; a.n_groups = n_groups; a.scale = scale;
+  a.invT = T > 0.f ? 1.f / T : 0.f;
+  a.tau = tau; a.table = table; a.lengths = lengths; a.ws = wp; a.part_rows = L.part_rows;
+  a.status = dev_status;
+  const int gate = !tau ? sd::NONE : T == 0.f ? sd::HARD : sd::SOFT;
+  const bool two = o_format == ETA_OUT_F32, d64 = dims->d == 64;
+  st = d64 ? sd::launch_attend_d<64>(gate, two, mq, mq1, mk, mv, a, P, s)
+           : sd::launch_attend_d<128>(gate, two, mq, mq1, mk, mv, a, P, s);
+  if (st != ETA_OK) return st;
+
+  const dim3 grid(dims->B * dims->Hq), block(sd::kCombine);
+  if (two)
+    return d64 ? launch_k(sd::shared_combine_kernel<64, float>, grid, block, 0, s, a,
+                          static_cast<float*>(o), lse)
+               : launch_k(sd::shared_combine_kernel<128, float>, grid, block, 0, s, a,
+                          static_cast<float*>(o), lse);
+  return d64 ? launch_k(sd::shared_combine_kernel<64, __nv_bfloat16>, grid, block, 0, s, a,
+                        static_cast<__nv_bfloat16*>(o), lse)
+             : launch_k(sd::shared_combine_kernel<128, __nv_bfloat16>, grid, block, 0, s, a,
+                        static_cast<__nv_bfloat16*>(o), lse);
+}
