@@ -170,14 +170,22 @@ def lib() -> C.CDLL:
     return L
 
 
-def _p(t: Optional[torch.Tensor]):
-    return None if t is None else C.c_void_p(t.data_ptr())
+# Pointers go as plain numbers: every entry point's argtypes are set, and a call of a
+# few microseconds should not spend one on wrapping them.
+def _p(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> Optional[C.c_void_p]:
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream) -> int:
     if stream is None:
+        # the current stream's handle without the Python object around it (3 us)
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return C.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _check(fn: str, code: int):

@@ -29,7 +29,7 @@ from . import _lib as L
 def _index_tensor(x, device) -> torch.Tensor:
     """int32 device tensor of a list, range or tensor of numbers."""
     if isinstance(x, torch.Tensor):
-        if x.dtype == torch.int32 and x.device == device and x.is_contiguous():
+        if x.dtype is torch.int32 and x.device == device and x.is_contiguous():
             return x
         return x.to(device=device, dtype=torch.int32).contiguous()
     return torch.tensor(list(x), dtype=torch.int32, device=device)
@@ -100,7 +100,7 @@ class PagedKVCache:
         [B + 1]; None: one token for every row)."""
         n_new = int(k_new.shape[0])
         for t in (k_new, v_new):
-            if (t.dtype != torch.bfloat16 or tuple(t.shape) != (n_new, self.Hkv, self.d)
+            if (t.dtype is not torch.bfloat16 or t.shape != (n_new, self.Hkv, self.d)
                     or not t.is_contiguous() or t.device != self.device):
                 raise ValueError(f"k_new/v_new must be contiguous bf16 [n_new, {self.Hkv}, "
                                  f"{self.d}] on {self.device}")
@@ -255,13 +255,13 @@ class PagedEtaDecoder:
 
     # -- attention ----------------------------------------------------------------------
     def _check_q(self, q):
-        if (q.dtype != torch.bfloat16 or tuple(q.shape) != (self.B, self.Hq, self.d)
+        if (q.dtype is not torch.bfloat16 or q.shape != (self.B, self.Hq, self.d)
                 or not q.is_contiguous() or q.device != self.device):
             raise ValueError(f"q must be contiguous bf16 [{self.B}, {self.Hq}, {self.d}] on "
                              f"{self.device}")
 
     def _check_tau(self, tau):
-        if (tau.dtype != torch.float32 or tuple(tau.shape) != (self.B, self.Hq)
+        if (tau.dtype is not torch.float32 or tau.shape != (self.B, self.Hq)
                 or not tau.is_contiguous() or tau.device != self.device):
             raise ValueError(f"tau must be contiguous fp32 [{self.B}, {self.Hq}] on "
                              f"{self.device}")

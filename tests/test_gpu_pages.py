@@ -67,7 +67,7 @@ class Both:
 
 
 @pytest.mark.parametrize("B,Hkv,d,blk", [(1, 1, 64, 64), (5, 2, 128, 64), (3, 4, 64, 128),
-                                         (70, 1, 128, 128)])
+                                         (70, 1, 128, 128), (1030, 1, 64, 64)])
 def test_append_fork_free_compact_in_random_order(B, Hkv, d, blk):
     t = Both(B, Hkv, d, blk, 5, 4 * B + 3, seed=B)
     rng = random.Random(B)
@@ -240,9 +240,10 @@ def test_compact_with_an_inconsistent_header_changes_nothing():
     assert torch.equal(t.c.K.cpu(), t.K)
 
 
-def test_many_chunks_of_pages():
+@pytest.mark.parametrize("n_pages", [2 * 4096 + 77, 8 * 4096 + 130])
+def test_many_chunks_of_pages(n_pages):
     """More pages than one CTA of the compaction's scan takes, ends inside a chunk."""
-    B, n_pages = 64, 2 * 4096 + 77
+    B = 64
     t = Both(B, 1, 64, 64, 160, n_pages, seed=5)
     rng = random.Random(3)
     t.append([rng.randint(1, 125 * 64) for _ in range(B)])
@@ -270,6 +271,44 @@ def test_copy_pages(d, Hkv, blk):
     torch.cuda.synchronize()
     assert int(c.dev_status) == L.DEVSTAT_BAD_ROW
     assert torch.equal(c.K, K) and torch.equal(c.V, V)
+
+
+def test_many_copies():
+    """More pairs than a CTA compares by itself."""
+    n_pages, n = 5000, 2200
+    c = PagedKVCache(1, 1, 64, 64, 1, n_pages)
+    gen = torch.Generator().manual_seed(6)
+    for x in (c.K, c.V):
+        x.copy_(torch.randn(x.shape, generator=gen).to(torch.bfloat16))
+    K, V = c.K.clone(), c.V.clone()
+    perm = torch.randperm(n_pages, generator=gen)
+    src, dst = perm[:n].clone(), perm[n:2 * n].clone()
+    c.copy_pages(src, dst)
+    K[dst.cuda()], V[dst.cuda()] = K[src.cuda()], V[src.cuda()]
+    torch.cuda.synchronize()
+    c.check_status()
+    assert torch.equal(c.K, K) and torch.equal(c.V, V)
+    dst[n - 1], dst[5], dst[7] = dst[0], src[3], -1      # refused, all three
+    c.K.copy_(V)
+    K = V.clone()
+    ok = torch.ones(n, dtype=torch.bool)
+    ok[[n - 1, 5, 7]] = False
+    c.copy_pages(src, dst)
+    K[dst[ok].cuda()] = K[src[ok].cuda()]
+    torch.cuda.synchronize()
+    assert int(c.dev_status) == L.DEVSTAT_BAD_ROW
+    assert torch.equal(c.K, K)
+
+
+def test_calls_leave_the_workspace_ready():
+    """Append, fork and free one after another many times: the count of finished CTAs and
+    the page bitmap are left as every call needs them."""
+    t = Both(12, 1, 64, 64, 40, 300)
+    for i in range(30):
+        t.append([(i * 7 + b) % 90 for b in range(6)] + [0] * 6)
+        t.fork(list(range(6)), list(range(6, 12)))
+        t.free([b for b in range(12) if (b + i) % 2 or b > 5])
+    t.check()
 
 
 def test_snapshot_and_graph_replay():
