@@ -51,11 +51,11 @@ using tc::tma_load_2d;
 constexpr int TILE = 128;                       // query rows and keys of a tile
 constexpr int SUB = 64;                         // keys of a TMA box (half a tile)
 constexpr int HALF = TILE * 128;                // [128 rows x 64 dims] bf16 = 16 KB
-constexpr int NKV = 2;                          // K/V ring stages
 constexpr int NSEG = 2;                         // segment records in flight
 constexpr int NT = 320;
 constexpr int kPlan = 1024;
 constexpr int kTmemCols = 512;
+constexpr uint32_t kIdleLimit = 1u << 24;       // polls of the MMA warp without an event
 constexpr float kRescale = 8.0f;                // rescale O when the max grows by > 8 (e^8)
 constexpr float kLog2e = 1.4426950408889634f;
 enum Gate { NONE = 0, HARD = 1, SOFT = 2 };
@@ -246,33 +246,50 @@ __global__ void __launch_bounds__(kPlan) shared_plan_kernel(const PlanParams p) 
 struct Seg {
   int live;             // 0: no more segments
   int pair;             // streams are two query tiles (else alternate key tiles of one)
-  int ntiles;
+  int ntiles, base;     // key tiles, and the CTA's running number of the first
   int row0;             // batch row of query row 0 of stream A
   int kvh;
   int mA, mB;           // valid query rows of the streams' tiles
   int partA, partB;     // first partial row of each stream
   int check;            // prefix: rows that do not share it are left out
+  int flip;             // single: the stream of the first key tile, and the query slot
+  int qph;              // bit s: the phase of query slot s that holds the segment's queries
 };
 
+// Jobs (key tiles) of stream x in a segment, and the tile of job j.
+ETA_DEV int jobs_of(const Seg& s, int x) {
+  return s.pair ? s.ntiles : (s.ntiles + 1 - (x ^ s.flip)) >> 1;
+}
+ETA_DEV int tile_of(const Seg& s, int x, int j) { return s.pair ? j : 2 * j + (x ^ s.flip); }
+
+template <int D>
 struct Misc {
-  uint64_t q_full, q_empty, kv_full[NKV], kv_empty[NKV];
+  static constexpr int NSLOT = D == 128 ? 5 : 10;
+  uint64_t q_full[2], q_empty[2], kv_full[NSLOT], kv_empty[NSLOT];
   uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
   uint64_t seg_full[NSEG], seg_empty[NSEG], fin;
   Seg seg[NSEG];
-  int2 nv[NKV];         // valid keys of the stage's two 64-key halves
+  int2 nv[NSLOT];       // of a V slot: valid keys of the tile's two 64-key halves
   uint32_t tmem_base;
   int abort_flag;
 };
 
+// Shared memory: two query tiles, then a ring of slots of one K or V tile each; tile T of
+// the CTA has its K in slot 2 T and its V in slot 2 T + 1, modulo the slots.  K and V are
+// apart because K is done with long before V: its slot loads again while the softmax runs.
 template <int D>
 struct Cfg {
   static constexpr int NH = D / 64;                     // 64-dim boxes
-  static constexpr int Q_TILE = NH * HALF;              // one query tile
-  static constexpr int STAGE = 2 * NH * HALF;           // K then V
+  static constexpr int SLOT = NH * HALF;                // one query, key or value tile
+  static constexpr int NSLOT = Misc<D>::NSLOT;
   static constexpr int OFF_Q = 0;                       // tiles A, B
-  static constexpr int OFF_KV = 2 * Q_TILE;
-  static constexpr int OFF_MISC = OFF_KV + NKV * STAGE;
-  static constexpr int SMEM = OFF_MISC + (int)sizeof(Misc) + 1024;
+  static constexpr int OFF_KV = 2 * SLOT;
+  static constexpr int OFF_MISC = OFF_KV + NSLOT * SLOT;
+  static constexpr int SMEM = OFF_MISC + (int)sizeof(Misc<D>) + 1024;
+  ETA_DEV static int kslot(int t) { return 2 * t % NSLOT; }
+  ETA_DEV static uint32_t kphase(int t) { return (uint32_t)(2 * t / NSLOT) & 1u; }
+  ETA_DEV static int vslot(int t) { return (2 * t + 1) % NSLOT; }
+  ETA_DEV static uint32_t vphase(int t) { return (uint32_t)((2 * t + 1) / NSLOT) & 1u; }
 };
 static_assert(Cfg<128>::SMEM <= 227 * 1024, "shared decode shared memory");
 
@@ -328,7 +345,27 @@ ETA_DEV void tmem_st32(uint32_t taddr, const uint32_t* v) {
       : "memory");
 }
 
-ETA_DEV void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+ETA_DEV void tmem_st16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+      "r"(v[15])
+      : "memory");
+}
+
+// Waits for the thread's loads; the 32 values are operands so that their use stays behind.
+ETA_DEV void tmem_wait_ld32(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                 "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
+                 "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]),
+                 "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
+                 "+f"(v[30]), "+f"(v[31])::"memory");
+}
+
 ETA_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 ETA_DEV float ex2_approx(float x) {             // 2^x on the SFU; -inf gives 0
@@ -357,10 +394,73 @@ ETA_DEV void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
       : "memory");
 }
 
-// Jobs of a segment, in the order the MMA warp takes them: job n belongs to stream n & 1;
-// pair: both streams take every key tile; else stream x takes the tiles of its parity.
-ETA_DEV int jobs_of(const Seg& s, int x) {
-  return s.pair ? s.ntiles : (s.ntiles + 1 - x) >> 1;
+// Whether phase `parity` of `bar` is over, without waiting.
+ETA_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// The gate on 32 scores of a query row, in raw units (see the softmax).
+struct GateArgs {
+  float tau_raw, ta, tb;
+};
+template <int GATE, int NS>
+ETA_DEV void gate32(float* v, const GateArgs& g) {
+  if constexpr (GATE == HARD) {
+    // a 1.0 / 0.0 flag and one packed multiply for two scores
+#pragma unroll
+    for (int u = 0; u < 32; u += 2) {
+      float f0, f1;
+      asm("set.ge.f32.f32 %0, %1, %2;" : "=f"(f0) : "f"(v[u]), "f"(g.tau_raw));
+      asm("set.ge.f32.f32 %0, %1, %2;" : "=f"(f1) : "f"(v[u + 1]), "f"(g.tau_raw));
+      const float2 y = __fmul2_rn(make_float2(v[u], v[u + 1]), make_float2(f0, f1));
+      v[u] = y.x;
+      v[u + 1] = y.y;
+    }
+  } else if constexpr (GATE == SOFT) {
+#pragma unroll
+    for (int u = 0; u < 32; ++u) {
+      if constexpr (NS == 1) {
+        const float hs = 0.5f * v[u];
+        v[u] = fmaf(hs, tanh_approx(fmaf(v[u], g.ta, -g.tb)), hs);
+      } else {
+        v[u] = __fdividef(v[u], 1.f + ex2_approx(fmaf(v[u], g.ta, -g.tb)));   // 0 once 2^x is inf
+      }
+    }
+  }
+}
+
+// Running maxima of 32 scores, in four independent chains.
+ETA_DEV void max32(const float* v, float* pm) {
+#pragma unroll
+  for (int u = 0; u < 32; u += 2) pm[(u >> 1) & 3] = fmax3(pm[(u >> 1) & 3], v[u], v[u + 1]);
+}
+
+// 32 weights e^(scale * (u - m)) = 2^(u * c1 + nm), summed into l2 and rounded to NS
+// bf16 terms, two keys a register.
+template <int NS>
+ETA_DEV void exp32(const float* v, float c1, float nm, float2& l2, uint32_t* hi, uint32_t* lo) {
+#pragma unroll
+  for (int u = 0; u < 16; ++u) {
+    const float2 a = __ffma2_rn(make_float2(v[2 * u], v[2 * u + 1]), make_float2(c1, c1),
+                                make_float2(nm, nm));
+    const float2 pr = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+    l2 = __fadd2_rn(l2, pr);
+    const __nv_bfloat162 hb = __floats2bfloat162_rn(pr.x, pr.y);
+    hi[u] = *reinterpret_cast<const uint32_t*>(&hb);
+    if constexpr (NS == 2) {
+      const float2 f = __bfloat1622float2(hb);
+      const __nv_bfloat162 lb = __floats2bfloat162_rn(pr.x - f.x, pr.y - f.y);
+      lo[u] = *reinterpret_cast<const uint32_t*>(&lb);
+    }
+  }
 }
 
 // GATE: Gate.  NS: the bf16 terms of P (1: bf16 output, 2: fp32 output).
@@ -374,18 +474,18 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Misc* ms = reinterpret_cast<Misc*>(smem + C::OFF_MISC);
+  Misc<D>* ms = reinterpret_cast<Misc<D>*>(smem + C::OFF_MISC);
   volatile int* abort_flag = &ms->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    mbar_init(&ms->q_full, 1);
-    mbar_init(&ms->q_empty, 1);
-    for (int s = 0; s < NKV; ++s) {
+    for (int s = 0; s < C::NSLOT; ++s) {
       mbar_init(&ms->kv_full[s], 1);
       mbar_init(&ms->kv_empty[s], 1);
     }
     for (int x = 0; x < 2; ++x) {
+      mbar_init(&ms->q_full[x], 1);
+      mbar_init(&ms->q_empty[x], 1);
       mbar_init(&ms->s_full[x], 1);
       mbar_init(&ms->p_full[x], 4);
       mbar_init(&ms->pv_done[x], 1);
@@ -418,7 +518,8 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
       const Head hd = *p.ws.head;
       const int a = blockIdx.x * hd.share, e = min(a + hd.share, hd.units);
       bool ok = true;
-      int nseg = 0, nst = 0;                     // segments, stages issued so far
+      int nseg = 0, slots = 0;                   // segments begun, K/V slots loaded so far
+      int qn[2] = {0, 0};                        // loads of each query slot so far
       int at = a < e ? p.ws.cta[blockIdx.x] : 0;
       int pos = a;
       while (ok) {
@@ -475,7 +576,10 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
             mrows = p.G;
           }
         }
-        // the record, then the queries, then the tiles
+        s.base = slots / 2;
+        s.flip = nseg & 1;
+        s.qph = (qn[0] & 1) | (qn[1] & 1) << 1;
+        // the record, then the first tile, the queries, and the other tiles
         const int sl = nseg % NSEG;
         if (!mbar_wait(&ms->seg_empty[sl], ((uint32_t)(nseg / NSEG) & 1u) ^ 1u, abort_flag)) {
           ok = false;
@@ -489,61 +593,57 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
           return key < key_end ? trow_p[key / p.blk] : -2;
         };
         int pg0 = page_at(key0), pg1 = page_at(key0 + SUB);
-        for (int t = 0; t < s.ntiles && ok; ++t, ++nst) {
-          const int st = nst % NKV, k0 = key0 + t * TILE;
-          const int c0 = pg0, c1 = pg1;
+        for (int t = 0; t < s.ntiles && ok; ++t) {
+          const int k0 = key0 + t * TILE;
+          const int pg[2] = {pg0, pg1};
           if (t + 1 < s.ntiles) {
             pg0 = page_at(k0 + TILE);
             pg1 = page_at(k0 + TILE + SUB);
           }
-          if (!mbar_wait(&ms->kv_empty[st], ((uint32_t)(nst / NKV) & 1u) ^ 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
           int nv[2] = {max(min(key_end - k0, SUB), 0), max(min(key_end - k0 - SUB, SUB), 0)};
-          const int pg[2] = {c0, c1};
 #pragma unroll
           for (int u = 0; u < 2; ++u)
             if (nv[u] > 0 && (pg[u] < 0 || pg[u] >= p.n_pages)) {
               set_status(p.status, ETA_DEVSTAT_BAD_BLOCK);
               nv[u] = 0;
             }
-          ms->nv[st] = make_int2(nv[0], nv[1]);
-          const int nbox = (nv[0] > 0) + (nv[1] > 0);
-          mbar_arrive_expect_tx(&ms->kv_full[st], (uint32_t)(nbox * 2 * C::NH * (HALF / 2)));
-          unsigned char* kd = smem + C::OFF_KV + st * C::STAGE;
-          unsigned char* vd = kd + C::NH * HALF;
+          const uint32_t bytes = (uint32_t)(((nv[0] > 0) + (nv[1] > 0)) * C::NH * (HALF / 2));
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            if (nv[u] == 0) continue;
-            const int key = k0 + u * SUB;
-            const int y = (pg[u] * p.Hkv + s.kvh) * p.blk + key % p.blk;
-#pragma unroll
-            for (int h = 0; h < C::NH; ++h)
-              tma_load_2d(kd + h * HALF + u * (HALF / 2), &tmK, h * 64, y, &ms->kv_full[st]);
-#pragma unroll
-            for (int h = 0; h < C::NH; ++h)
-              tma_load_2d(vd + h * HALF + u * (HALF / 2), &tmV, h * 64, y, &ms->kv_full[st]);
-          }
-          if (t == 0) {
-            // the queries of the previous segment have been read by its last Q K^T
-            if (!mbar_wait(&ms->q_empty, ((uint32_t)nseg & 1u) ^ 1u, abort_flag)) {
+          for (int v = 0; v < 2 && ok; ++v) {    // K, then V
+            const int st = slots % C::NSLOT;
+            if (!mbar_wait(&ms->kv_empty[st], ((uint32_t)(slots / C::NSLOT) & 1u) ^ 1u,
+                           abort_flag)) {
               ok = false;
-              ++nst;
               break;
             }
-            const uint32_t bytes = (uint32_t)(mrows * 128 * C::NH) * (s.pair ? 2 : 1);
-            mbar_arrive_expect_tx(&ms->q_full, bytes);
+            if (v) ms->nv[st] = make_int2(nv[0], nv[1]);
+            mbar_arrive_expect_tx(&ms->kv_full[st], bytes);
+            unsigned char* to = smem + C::OFF_KV + st * C::SLOT;
 #pragma unroll
-            for (int h = 0; h < C::NH; ++h) {
-              unsigned char* qd = smem + C::OFF_Q + h * HALF;
-              if (s.check) {
-                tma_load_3d(qd, &tmQ, h * 64, s.kvh * p.G, s.row0, &ms->q_full);
-                if (s.pair)
-                  tma_load_3d(qd + C::Q_TILE, &tmQ, h * 64, s.kvh * p.G, s.row0 + TILE / p.G,
-                              &ms->q_full);
-              } else {
-                tma_load_3d(qd, &tmQ1, h * 64, s.kvh * p.G, s.row0, &ms->q_full);
+            for (int u = 0; u < 2; ++u) {
+              if (nv[u] == 0) continue;
+              const int y = (pg[u] * p.Hkv + s.kvh) * p.blk + (k0 + u * SUB) % p.blk;
+#pragma unroll
+              for (int h = 0; h < C::NH; ++h)
+                tma_load_2d(to + h * HALF + u * (HALF / 2), v ? &tmV : &tmK, h * 64, y,
+                            &ms->kv_full[st]);
+            }
+            ++slots;
+            if (t == 0 && v == 0) {
+              // query slots: a pair fills both, a single segment the one of its number
+              for (int x = 0; x < 2 && ok; ++x) {
+                if (!s.pair && x != s.flip) continue;
+                if (!mbar_wait(&ms->q_empty[x], ((uint32_t)qn[x] & 1u) ^ 1u, abort_flag)) {
+                  ok = false;
+                  break;
+                }
+                mbar_arrive_expect_tx(&ms->q_full[x], (uint32_t)(mrows * 128 * C::NH));
+                ++qn[x];
+                const int row = s.row0 + (s.pair && x ? TILE / p.G : 0);
+#pragma unroll
+                for (int h = 0; h < C::NH; ++h)
+                  tma_load_3d(smem + C::OFF_Q + x * C::SLOT + h * HALF, s.check ? &tmQ : &tmQ1,
+                              h * 64, s.kvh * p.G, row, &ms->q_full[x]);
               }
             }
           }
@@ -555,86 +655,129 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
         // wait (bounded) for every copy this thread issued before the CTA exits
         set_status(p.status, ETA_DEVSTAT_TIMEOUT);
         *abort_flag = 1;
-        for (int k = max(0, nst - NKV); k < nst; ++k)
-          mbar_wait(&ms->kv_full[k % NKV], (uint32_t)(k / NKV) & 1u, nullptr);
-        if (nseg > 0) mbar_wait(&ms->q_full, (uint32_t)(nseg - 1) & 1u, nullptr);
-        mbar_wait_n(&ms->q_full, (uint32_t)nseg & 1u, nullptr, 1u << 16);
+        for (int k = max(0, slots - C::NSLOT); k < slots; ++k)
+          mbar_wait(&ms->kv_full[k % C::NSLOT], (uint32_t)(k / C::NSLOT) & 1u, nullptr);
+        for (int x = 0; x < 2; ++x)
+          if (qn[x] > 0) mbar_wait(&ms->q_full[x], (uint32_t)(qn[x] - 1) & 1u, nullptr);
       }
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------------ MMA issuer
+    // Event driven: each stream steps through its segments by itself, Q K^T once its S
+    // columns (P of the job before) are free, P V once the softmax has written P; one
+    // stream's wait never holds up the other.
     if (lane == 0) {
+      Seg s[2];
+      int nseg[2] = {0, 0}, jobs[2] = {0, 0};    // the stream's segment, and its jobs there
+      int qk[2] = {0, 0}, pv[2] = {0, 0};        // of which issued
+      int cnt[2] = {0, 0}, used[2] = {0, 0};     // jobs, and segments with jobs, before it
+      int left[NSEG][2], both[NSEG];             // per segment: Q K^T to come, streams done
+      bool open[2] = {false, false}, over[2] = {false, false};
+#pragma unroll
+      for (int r = 0; r < NSEG; ++r) left[r][0] = left[r][1] = both[r] = 0;
+      const uint32_t q0 = smem_u32(smem + C::OFF_Q), kv0 = smem_u32(smem + C::OFF_KV);
       bool ok = true;
-      int nseg = 0, nst = 0;                     // segments done; stage of their next tile
-      int cnt[2] = {0, 0};                       // jobs done per stream
-      int used[2] = {0, 0};                      // segments in which a stream had jobs
-      const uint32_t qa[2] = {smem_u32(smem + C::OFF_Q), smem_u32(smem + C::OFF_Q + C::Q_TILE)};
-      for (;; ++nseg) {
-        const int sl = nseg % NSEG;
-        if (!mbar_wait(&ms->seg_full[sl], (uint32_t)(nseg / NSEG) & 1u, abort_flag)) {
-          ok = false;
-          break;
-        }
-        const Seg s = ms->seg[sl];
-        if (!s.live) break;
-        if (!mbar_wait(&ms->q_full, (uint32_t)nseg & 1u, abort_flag)) { ok = false; break; }
-        const int jobs = s.pair ? 2 * s.ntiles : s.ntiles;
-        const int base[2] = {cnt[0], cnt[1]};
-        auto tile_of = [&](int n) { return s.pair ? n >> 1 : n; };
-        auto issue_qk = [&](int n) -> bool {     // S_x = Q_x K^T
-          const int x = n & 1, k = base[x] + (n >> 1), st = (nst + tile_of(n)) % NKV;
-          const uint32_t ph = (uint32_t)((nst + tile_of(n)) / NKV) & 1u;
-          if (!mbar_wait(&ms->kv_full[st], ph, abort_flag)) return false;
-          // S_x's columns hold P_x of the stream's previous job until P V has read it
-          if (k > 0 && !mbar_wait(&ms->pv_done[x], (uint32_t)(k - 1) & 1u, abort_flag)) return false;
-          tc_fence_after();
-          const uint32_t ka = smem_u32(smem + C::OFF_KV + st * C::STAGE);
-          const uint32_t qx = qa[s.pair ? x : 0];
+      uint32_t idle = 0;
+      while (ok && !(over[0] && over[1])) {
+        bool did = false;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (uint32_t)(kk >> 2) * HALF + (uint32_t)(kk & 3) * 32;
-            mma_f16(tS[x], smem_desc(qx + off, 16, 1024, tc::kSwizzle128),
-                    smem_desc(ka + off, 16, 1024, tc::kSwizzle128), idesc<TILE>(), kk > 0);
-          }
-          mma_commit(&ms->s_full[x]);
-          if (n == jobs - 1) mma_commit(&ms->q_empty);   // the segment's last Q K^T
-          return true;
-        };
-        auto issue_pv = [&](int n) -> bool {     // O_x += P_x V
-          const int x = n & 1, k = base[x] + (n >> 1), st = (nst + tile_of(n)) % NKV;
-          if (!mbar_wait(&ms->p_full[x], (uint32_t)k & 1u, abort_flag)) return false;
-          // a segment's first P V overwrites O_x: the last one's has to be read out
-          if (n < 2 && used[x] > 0 &&
-              !mbar_wait(&ms->o_free[x], (uint32_t)(used[x] - 1) & 1u, abort_flag))
-            return false;
-          tc_fence_after();
-          const uint32_t va = smem_u32(smem + C::OFF_KV + st * C::STAGE + C::NH * HALF);
-          constexpr uint32_t id = idesc<D>() | (1u << 16);           // V is MN-major
-#pragma unroll
-          for (int term = 0; term < NS; ++term)
-#pragma unroll
-            for (int kk = 0; kk < TILE / 16; ++kk)
-              mma_f16_ts(tO[x], tS[x] + term * 64 + kk * 8,
-                         smem_desc(va + kk * 2048, HALF, 1024, tc::kSwizzle128), id,
-                         (n >= 2 || term > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(&ms->pv_done[x]);
-          if (!s.pair || x == 1) mma_commit(&ms->kv_empty[st]);
-          return true;
-        };
-        ok = issue_qk(0);
-        if (ok && jobs > 1) ok = issue_qk(1);
-        for (int n = 0; n < jobs && ok; ++n) {
-          ok = issue_pv(n);
-          if (ok && n + 2 < jobs) ok = issue_qk(n + 2);
-        }
-        if (!ok) break;
         for (int x = 0; x < 2; ++x) {
-          const int j = jobs_of(s, x);
-          cnt[x] += j;
-          used[x] += j > 0;
+          if (over[x]) continue;
+          if (!open[x]) {                        // the stream's next segment
+            const int sl = nseg[x] % NSEG;
+            if (!mbar_test(&ms->seg_full[sl], (uint32_t)(nseg[x] / NSEG) & 1u)) continue;
+            s[x] = ms->seg[sl];
+            did = true;
+            if (!s[x].live) {
+              over[x] = true;
+              continue;
+            }
+            jobs[x] = jobs_of(s[x], x);
+            qk[x] = pv[x] = 0;
+            open[x] = true;
+            if (nseg[x ^ 1] <= nseg[x] && !(open[x ^ 1] && nseg[x ^ 1] == nseg[x])) {
+              // the first of the two streams to get here
+#pragma unroll
+              for (int r = 0; r < NSEG; ++r)
+                if (r == sl) {
+                  left[r][0] = s[x].pair ? s[x].ntiles : s[x].flip == 0 ? s[x].ntiles : 0;
+                  left[r][1] = s[x].pair ? s[x].ntiles : s[x].flip == 1 ? s[x].ntiles : 0;
+                  both[r] = 0;
+                }
+            }
+          }
+          const int sl = nseg[x] % NSEG;
+          // P V of the oldest job whose S is out
+          if (pv[x] < qk[x] && mbar_test(&ms->p_full[x], (uint32_t)(cnt[x] + pv[x]) & 1u) &&
+              (pv[x] > 0 || used[x] == 0 ||
+               mbar_test(&ms->o_free[x], (uint32_t)(used[x] - 1) & 1u))) {
+            const int tile = tile_of(s[x], x, pv[x]), T = s[x].base + tile;
+            // long over, the softmax waited for it: makes V visible to this thread
+            if (!mbar_test(&ms->kv_full[C::vslot(T)], C::vphase(T))) continue;
+            tc_fence_after();
+            const uint32_t va = kv0 + C::vslot(T) * C::SLOT;
+            constexpr uint32_t id = idesc<D>() | (1u << 16);           // V is MN-major
+#pragma unroll
+            for (int term = 0; term < NS; ++term)
+#pragma unroll
+              for (int kk = 0; kk < TILE / 16; ++kk)
+                mma_f16_ts(tO[x],
+                           tS[x] + (NS == 1 ? kk * 8 : (kk >> 1) * 32 + term * 16 + (kk & 1) * 8),
+                           smem_desc(va + kk * 2048, HALF, 1024, tc::kSwizzle128), id,
+                           (pv[x] > 0 || term > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(&ms->pv_done[x]);
+            ++pv[x];
+            // a pair's tile is done with when both streams have taken it
+            if (!s[x].pair || nseg[x ^ 1] > nseg[x] ||
+                (open[x ^ 1] && nseg[x ^ 1] == nseg[x] && pv[x ^ 1] > tile))
+              mma_commit(&ms->kv_empty[C::vslot(T)]);
+            did = true;
+          }
+          // Q K^T of the next job
+          if (qk[x] < jobs[x] && qk[x] == pv[x] &&
+              (cnt[x] + qk[x] == 0 ||
+               mbar_test(&ms->pv_done[x], (uint32_t)(cnt[x] + qk[x] - 1) & 1u))) {
+            const int tile = tile_of(s[x], x, qk[x]), T = s[x].base + tile;
+            const int qs = s[x].pair ? x : s[x].flip;
+            if (mbar_test(&ms->kv_full[C::kslot(T)], C::kphase(T)) &&
+                mbar_test(&ms->q_full[qs], (uint32_t)(s[x].qph >> qs) & 1u)) {
+              tc_fence_after();
+              const uint32_t ka = kv0 + C::kslot(T) * C::SLOT, qa = q0 + qs * C::SLOT;
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (uint32_t)(kk >> 2) * HALF + (uint32_t)(kk & 3) * 32;
+                mma_f16(tS[x], smem_desc(qa + off, 16, 1024, tc::kSwizzle128),
+                        smem_desc(ka + off, 16, 1024, tc::kSwizzle128), idesc<TILE>(), kk > 0);
+              }
+              mma_commit(&ms->s_full[x]);
+              ++qk[x];
+              if (!s[x].pair || nseg[x ^ 1] > nseg[x] ||
+                  (open[x ^ 1] && nseg[x ^ 1] == nseg[x] && qk[x ^ 1] > tile))
+                mma_commit(&ms->kv_empty[C::kslot(T)]);
+#pragma unroll
+              for (int r = 0; r < NSEG; ++r)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                  if (r == sl && y == qs && --left[r][y] == 0) mma_commit(&ms->q_empty[y]);
+              did = true;
+            }
+          }
+          if (pv[x] == jobs[x]) {                // on to the next segment
+            cnt[x] += jobs[x];
+            used[x] += jobs[x] > 0;
+            ++nseg[x];
+            open[x] = false;
+#pragma unroll
+            for (int r = 0; r < NSEG; ++r)
+              if (r == sl && ++both[r] == 2) mbar_arrive(&ms->seg_empty[r]);
+            did = true;
+          }
         }
-        nst += s.ntiles;
-        mbar_arrive(&ms->seg_empty[sl]);
+        if (did) {
+          idle = 0;
+        } else if (++idle > kIdleLimit || *abort_flag) {
+          ok = false;
+        }
       }
       if (!ok) {
         set_status(p.status, ETA_DEVSTAT_TIMEOUT);
@@ -652,7 +795,7 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
     const float c1 = p.scale * kLog2e;
     const float resc_raw = kRescale / p.scale;
     bool ok = true;
-    int nseg = 0, nst = 0, cnt = 0;
+    int nseg = 0, cnt = 0;
     auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
     };
@@ -662,6 +805,7 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
       const Seg s = ms->seg[sl];
       if (!s.live) break;
       const int mine = x == 0 ? s.mA : s.mB;
+      const bool active = (warp & 3) * 32 < mine;      // the warp has a valid row
       const int b = s.row0 + (i + (s.pair && x ? TILE : 0)) / p.G, h = s.kvh * p.G + i % p.G;
       const bool valid = i < mine;
       // Gated logits in raw units u (the gated logit is scale * u), so that the scale
@@ -670,51 +814,31 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
       // transcendental a key, 2^-11 off, below the output's own rounding), and
       // s / (1 + 2^(s * ta - tb)) for an fp32 one; and e^(scale * (u - m)) is
       // 2^(u * c1 - m * c1), c1 = scale * log2(e).
-      float tau_raw = 0.f, ta = 0.f, tb = 0.f;
+      GateArgs ga = {};
       if constexpr (GATE != NONE) {
         const float tau = valid ? p.tau[(size_t)b * p.Hq + h] : 0.f;
-        tau_raw = tau / p.scale;
         const float f = (NS == 1 ? 0.5f : -kLog2e) * p.invT;
-        ta = p.scale * f;
-        tb = tau * f;
+        ga.tau_raw = tau / p.scale;
+        ga.ta = p.scale * f;
+        ga.tb = tau * f;
       }
       float m = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
       const int jobs = jobs_of(s, x);
       for (int j = 0; j < jobs; ++j, ++cnt) {
-        const int st = (nst + (s.pair ? j : 2 * j + x)) % NKV;
-        const uint32_t ph = (uint32_t)((nst + (s.pair ? j : 2 * j + x)) / NKV) & 1u;
-        if (!wwait(&ms->s_full[x], (uint32_t)cnt & 1u) || !wwait(&ms->kv_full[st], ph)) {
+        const int T = s.base + tile_of(s, x, j);
+        // V's slot is not loaded again before this tile's P V: its phase is this tile's
+        if (!wwait(&ms->s_full[x], (uint32_t)cnt & 1u) ||
+            !wwait(&ms->kv_full[C::vslot(T)], C::vphase(T))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const int2 nv = ms->nv[st];
-        float sv[TILE];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tSx + c * 32, sv + c * 32);
-        tmem_wait_ld();
-        if constexpr (GATE == HARD) {
-#pragma unroll
-          for (int c = 0; c < TILE; ++c) sv[c] = sv[c] >= tau_raw ? sv[c] : 0.f;
-        } else if constexpr (GATE == SOFT) {
-#pragma unroll
-          for (int c = 0; c < TILE; ++c) {
-            if constexpr (NS == 1) {
-              const float hs = 0.5f * sv[c];
-              sv[c] = fmaf(hs, tanh_approx(fmaf(sv[c], ta, -tb)), hs);
-            } else {
-              sv[c] = __fdividef(sv[c], 1.f + ex2_approx(fmaf(sv[c], ta, -tb)));   // 0 once 2^x is inf
-            }
-          }
-        }
-        if (nv.x < SUB || nv.y < SUB) {          // keys past the end
-#pragma unroll
-          for (int c = 0; c < TILE; ++c)
-            if ((c & (SUB - 1)) >= (c < SUB ? nv.x : nv.y)) sv[c] = -INFINITY;
-          // their V rows must be finite for P V
+        const int2 nv = ms->nv[C::vslot(T)];
+        const bool partial = nv.x < SUB || nv.y < SUB;
+        if (partial) {                           // V rows past the end must be finite
           if ((i & (SUB - 1)) >= (i < SUB ? nv.x : nv.y)) {
-            unsigned char* vt = smem + C::OFF_KV + st * C::STAGE + C::NH * HALF + i * 128;
+            unsigned char* vt = smem + C::OFF_KV + C::vslot(T) * C::SLOT + i * 128;
 #pragma unroll
             for (int hh = 0; hh < C::NH; ++hh)
 #pragma unroll
@@ -723,96 +847,133 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
           }
           fence_async_smem();
         }
-        float pm[8];
+        if (active) {
+          uint32_t P[NS == 1 ? 64 : 1];
+          bool again = NS == 2 || j == 0 || partial;
+          if constexpr (NS == 1) {
+            // One pass with the maximum of the tiles before: a weight may exceed 1, by
+            // e^kRescale at most; if any does by more the tile is done again below (S is
+            // still there: P waits in registers).
+            if (!again) {
+              float va[32], vb[32], pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+              float2 ln = l2;
+              const float nm = m == -INFINITY ? 0.f : -m * c1;
+              tmem_ld32(tSx, va);
+              tmem_wait_ld32(va);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) pm[u] = fmax3(sv[2 * u], sv[2 * u + 1], sv[16 + 2 * u]);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) pm[u] = fmaxf(pm[u], sv[17 + 2 * u]);
-#pragma unroll
-        for (int c = 32; c < TILE; c += 2)
-          pm[(c >> 1) & 7] = fmax3(pm[(c >> 1) & 7], sv[c], sv[c + 1]);
-        const float mx = fmaxf(fmax3(fmax3(pm[0], pm[1], pm[2]), pm[3], pm[4]),
-                               fmax3(pm[5], pm[6], pm[7]));
-        // the first tile sets the maximum; later ones rescale O (in TMEM) only when it
-        // grew by more than kRescale
-        float alpha = 1.f;
-        bool resc = false;
-        if (m == -INFINITY) {
-          m = mx;
-        } else if (mx > m + resc_raw) {
-          alpha = ex2_approx((m - mx) * c1);
-          m = mx;
-          resc = true;
-        }
-        if (__any_sync(0xffffffffu, resc)) {
-          // P V of the stream's previous job is complete: this job's Q K^T waited for it
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            float ov[32];
-            tmem_ld32(tOx + c * 32, ov);
-            tmem_wait_ld();
-            uint32_t w[32];
-#pragma unroll
-            for (int u = 0; u < 32; ++u) w[u] = __float_as_uint(ov[u] * alpha);
-            tmem_st32(tOx + c * 32, w);
-          }
-          l2.x *= alpha;
-          l2.y *= alpha;
-        }
-        const float nm = m == -INFINITY ? 0.f : -m * c1;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t hi[32], lo[32];
-#pragma unroll
-          for (int u = 0; u < 32; ++u) {
-            const int k = c * 64 + 2 * u;
-            const float2 a = __ffma2_rn(make_float2(sv[k], sv[k + 1]), make_float2(c1, c1),
-                                        make_float2(nm, nm));
-            const float2 pr = make_float2(ex2_approx(a.x), ex2_approx(a.y));
-            l2 = __fadd2_rn(l2, pr);
-            const __nv_bfloat162 hb = __floats2bfloat162_rn(pr.x, pr.y);
-            hi[u] = *reinterpret_cast<const uint32_t*>(&hb);
-            if constexpr (NS == 2) {
-              const float2 f = __bfloat1622float2(hb);
-              const __nv_bfloat162 lb = __floats2bfloat162_rn(pr.x - f.x, pr.y - f.y);
-              lo[u] = *reinterpret_cast<const uint32_t*>(&lb);
+              for (int c = 0; c < 4; ++c) {
+                float* v = c & 1 ? vb : va;
+                float* w = c & 1 ? va : vb;
+                if (c < 3) tmem_ld32(tSx + (c + 1) * 32, w);
+                gate32<GATE, NS>(v, ga);
+                max32(v, pm);
+                exp32<1>(v, c1, nm, ln, P + 16 * c, nullptr);
+                if (c < 3) tmem_wait_ld32(w);
+              }
+              const float mx = fmaxf(fmax3(pm[0], pm[1], pm[2]), pm[3]);
+              again = __any_sync(0xffffffffu, valid && mx > m + resc_raw);
+              if (!again) l2 = ln;
             }
           }
-          tmem_st32(tSx + c * 32, hi);
-          if constexpr (NS == 2) tmem_st32(tSx + 64 + c * 32, lo);
+          if (again) {
+            // the tile's maximum first; gated and masked scores go back into S
+            float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float v[32];
+              tmem_ld32(tSx + c * 32, v);
+              tmem_wait_ld32(v);
+              gate32<GATE, NS>(v, ga);
+              if (partial) {
+                const int lim = (c < 2 ? nv.x : nv.y) - (c & 1) * 32;
+#pragma unroll
+                for (int u = 0; u < 32; ++u)
+                  if (u >= lim) v[u] = -INFINITY;
+              }
+              max32(v, pm);
+              if (GATE != NONE || partial)
+                tmem_st32(tSx + c * 32, reinterpret_cast<const uint32_t*>(v));
+            }
+            const float mx = fmaxf(fmax3(pm[0], pm[1], pm[2]), pm[3]);
+            if (GATE != NONE || partial) tmem_wait_st();
+            // the first tile sets the maximum; later ones rescale O (in TMEM) only when it
+            // grew by more than kRescale
+            float alpha = 1.f;
+            bool resc = false;
+            if (m == -INFINITY) {
+              m = mx;
+            } else if (mx > m + resc_raw) {
+              alpha = ex2_approx((m - mx) * c1);
+              m = mx;
+              resc = true;
+            }
+            if (__any_sync(0xffffffffu, resc)) {
+              // P V of the stream's previous job is complete: this Q K^T waited for it
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                float ov[32];
+                tmem_ld32(tOx + c * 32, ov);
+                tmem_wait_ld32(ov);
+#pragma unroll
+                for (int u = 0; u < 32; ++u) ov[u] *= alpha;
+                tmem_st32(tOx + c * 32, reinterpret_cast<const uint32_t*>(ov));
+              }
+              l2.x *= alpha;
+              l2.y *= alpha;
+            }
+            const float nm = m == -INFINITY ? 0.f : -m * c1;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float v[32];
+              tmem_ld32(tSx + c * 32, v);
+              tmem_wait_ld32(v);
+              if constexpr (NS == 1) {
+                exp32<1>(v, c1, nm, l2, P + 16 * c, nullptr);
+              } else {                           // both terms into the chunk's own columns
+                uint32_t hi[16], lo[16];
+                exp32<2>(v, c1, nm, l2, hi, lo);
+                tmem_st16(tSx + c * 32, hi);
+                tmem_st16(tSx + c * 32 + 16, lo);
+              }
+            }
+          }
+          if constexpr (NS == 1) {
+            tmem_st32(tSx, P);
+            tmem_st32(tSx + 32, P + 32);
+          }
+          tmem_wait_st();
         }
-        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms->p_full[x]);
       }
       if (!ok) break;
-      nst += s.ntiles;
       // the segment's partial result of this stream
       if (jobs > 0) {
         if (!wwait(&ms->pv_done[x], (uint32_t)(cnt - 1) & 1u)) { ok = false; break; }
         tc_fence_after();
       }
-      const bool store = valid && (!s.check || p.ws.row[b].start > 0) &&
-                         ETA_IN_BOUNDS((x ? s.partB : s.partA) + i, p.part_rows, p.status);
-      const size_t slot = (size_t)((x ? s.partB : s.partA) + i);
-      if (jobs > 0) {
+      if (active) {
+        const int part = (x ? s.partB : s.partA) + i;
+        const bool store = valid && (!s.check || p.ws.row[b].start > 0) &&
+                           ETA_IN_BOUNDS(part, p.part_rows, p.status);
+        if (jobs > 0) {
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          float ov[32];
-          tmem_ld32(tOx + c * 32, ov);
-          tmem_wait_ld();
-          if (store) {
-            float4* to = reinterpret_cast<float4*>(p.ws.part_o + slot * D + c * 32);
+          for (int c = 0; c < D / 32; ++c) {
+            float ov[32];
+            tmem_ld32(tOx + c * 32, ov);
+            tmem_wait_ld32(ov);
+            if (store) {
+              float4* to = reinterpret_cast<float4*>(p.ws.part_o + (size_t)part * D + c * 32);
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-              to[u] = make_float4(ov[4 * u], ov[4 * u + 1], ov[4 * u + 2], ov[4 * u + 3]);
+              for (int u = 0; u < 8; ++u)
+                to[u] = make_float4(ov[4 * u], ov[4 * u + 1], ov[4 * u + 2], ov[4 * u + 3]);
+            }
           }
         }
+        if (store)
+          reinterpret_cast<float2*>(p.ws.part_ml)[part] = make_float2(m * p.scale, l2.x + l2.y);
       }
-      if (store)
-        reinterpret_cast<float2*>(p.ws.part_ml)[slot] =
-            make_float2(m * p.scale, l2.x + l2.y);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
