@@ -51,7 +51,7 @@ using tc::tma_load_2d;
 constexpr int TILE = 128;                       // query rows and keys of a tile
 constexpr int SUB = 64;                         // keys of a TMA box (half a tile)
 constexpr int HALF = TILE * 128;                // [128 rows x 64 dims] bf16 = 16 KB
-constexpr int NSEG = 2;                         // segment records in flight
+constexpr int NSEG = 4;                         // segment records in flight
 constexpr int NT = 320;
 constexpr int kPlan = 1024;
 constexpr int kTmemCols = 512;
@@ -74,21 +74,27 @@ struct GroupRec {
 };
 
 struct RowRec {
-  int off;        // first unit, after all prefix units
+  int off;        // first unit, counted behind all prefix units
   int nt;         // units per KV head
   int start;      // first block that the row reads by itself
   int group;      // the group it shares a prefix with, or -1
 };
 
 struct Head {
-  int prefix_units, units, share, suffix_base;
+  int share, suffix_base;
+};
+
+// What a CTA begins with: its units [a, e), the item of unit a (the group, or n_groups +
+// row), and where the rows' own units begin.
+struct CtaRec {
+  int a, e, item, prefix_units;
 };
 
 struct Ws {
   Head* head;
   GroupRec* grp;
   RowRec* row;
-  int32_t* cta;         // per CTA: the group (or n_groups + row) of its first unit
+  CtaRec* cta;
   float* part_ml;
   float* part_o;
 };
@@ -100,38 +106,33 @@ struct PlanParams {
   int32_t* status;
 };
 
-template <typename T>
-ETA_DEV T cta_scan(T v, T* wsum, T& total) {    // exclusive, over kPlan threads
+ETA_DEV int2 add2(int2 a, int2 b) { return make_int2(a.x + b.x, a.y + b.y); }
+
+ETA_DEV int2 cta_scan(int2 v, int2* wsum, int2& total) {   // exclusive, over kPlan threads
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  T incl = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const T y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) wsum[warp] = incl;
-  __syncthreads();
-  if (warp == 0) {
-    const T w = wsum[lane];
-    T wi = w;
+  auto incl_scan = [&](int2 x) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const T y = __shfl_up_sync(0xffffffffu, wi, o);
-      if (lane >= o) wi += y;
+      const int2 y = make_int2(__shfl_up_sync(0xffffffffu, x.x, o),
+                               __shfl_up_sync(0xffffffffu, x.y, o));
+      if (lane >= o) x = add2(x, y);
     }
-    wsum[lane] = wi - w;
-    if (lane == 31) wsum[32] = wi;
-  }
+    return x;
+  };
+  const int2 incl = incl_scan(v);
+  __syncthreads();                              // wsum's last readers are done
+  if (lane == 31) wsum[warp] = incl;
   __syncthreads();
-  const T r = wsum[warp] + incl - v;
-  total = wsum[32];
-  __syncthreads();
-  return r;
+  const int2 w = incl_scan(wsum[lane]);         // every warp alike
+  total = make_int2(__shfl_sync(0xffffffffu, w.x, 31), __shfl_sync(0xffffffffu, w.y, 31));
+  const int2 before = make_int2(__shfl_sync(0xffffffffu, w.x, (warp + 31) & 31),
+                                __shfl_sync(0xffffffffu, w.y, (warp + 31) & 31));
+  return make_int2((warp ? before.x : 0) + incl.x - v.x, (warp ? before.y : 0) + incl.y - v.y);
 }
 
 __global__ void __launch_bounds__(kPlan) shared_plan_kernel(const PlanParams p) {
   ETA_PDL_ENTRY();
-  __shared__ int wsum[33];
+  __shared__ int2 wsum[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cap = p.NB * p.blk;
   bool bad = false;
@@ -146,8 +147,8 @@ __global__ void __launch_bounds__(kPlan) shared_plan_kernel(const PlanParams p) 
     if (len < 0 || len > cap) set_status(p.status, ETA_DEVSTAT_BAD_LENGTH);
   }
   bad = __syncthreads_or(bad);
-  if (bad) set_status(p.status, ETA_DEVSTAT_BAD_ROW);
-  else if (threadIdx.x == 0 && (p.group_off[0] != 0 || p.group_off[p.n_groups] != p.B))
+  if (threadIdx.x == 0 &&
+      (bad || p.group_off[0] != 0 || p.group_off[p.n_groups] != p.B))
     set_status(p.status, ETA_DEVSTAT_BAD_ROW);
   // a warp per group: who shares, and whose table is read
   for (int g = warp; g < p.n_groups; g += kPlan / 32) {
@@ -189,57 +190,63 @@ __global__ void __launch_bounds__(kPlan) shared_plan_kernel(const PlanParams p) 
     }
   }
   __syncthreads();
-  int carry = 0, total;
-  for (int g0 = 0; g0 < p.n_groups; g0 += kPlan) {
-    const int g = g0 + threadIdx.x;
-    int n = 0;
-    if (g < p.n_groups) n = p.Hkv * p.ws.grp[g].npairs * p.ws.grp[g].nt;
-    const int off = carry + cta_scan(n, wsum, total);
-    if (g < p.n_groups) p.ws.grp[g].off = off;
-    carry += total;
-  }
-  const int prefix_units = carry;
-  for (int b0 = 0; b0 < p.B; b0 += kPlan) {
-    const int b = b0 + threadIdx.x;
-    int nt = 0;
-    if (b < p.B) {
-      const int len = min(max(p.lengths[b], 0), cap);
-      nt = (max(len - p.ws.row[b].start * p.blk, 0) + TILE - 1) / TILE;
-      p.ws.row[b].nt = nt;
+  // first units: of the groups (x) and of the rows (y, counted from zero)
+  int2 carry = make_int2(0, 0), total;
+  for (int i0 = 0; i0 < max(p.n_groups, p.B); i0 += kPlan) {
+    const int i = i0 + threadIdx.x;
+    int2 n = make_int2(0, 0);
+    if (i < p.n_groups) n.x = p.Hkv * p.ws.grp[i].npairs * p.ws.grp[i].nt;
+    if (i < p.B) {
+      const int len = min(max(p.lengths[i], 0), cap);
+      const int nt = (max(len - p.ws.row[i].start * p.blk, 0) + TILE - 1) / TILE;
+      p.ws.row[i].nt = nt;
+      n.y = p.Hkv * nt;
     }
-    const int off = carry + cta_scan(nt * p.Hkv, wsum, total);
-    if (b < p.B) p.ws.row[b].off = off;
-    carry += total;
+    const int2 off = add2(carry, cta_scan(n, wsum, total));
+    if (i < p.n_groups) p.ws.grp[i].off = off.x;
+    if (i < p.B) p.ws.row[i].off = off.y;
+    carry = add2(carry, total);
   }
-  const int units = carry;
+  const int prefix_units = carry.x, units = carry.x + carry.y;
   const int share = max((units + p.P - 1) / p.P, 1);
-  // the item that every CTA starts in, and where a group's partial results go
-  carry = 0;
+  for (int c = threadIdx.x; c < p.P; c += kPlan) {
+    p.ws.cta[c].a = min(c * share, units);
+    p.ws.cta[c].e = min(c * share + share, units);
+    p.ws.cta[c].prefix_units = prefix_units;
+  }
+  // where a group's partial results go
+  carry = make_int2(0, 0);
   for (int g0 = 0; g0 < p.n_groups; g0 += kPlan) {
     const int g = g0 + threadIdx.x;
-    int rows = 0, n = 0, off = 0, cf = 0;
+    int2 rows = make_int2(0, 0);
+    int cf = 0;
     if (g < p.n_groups) {
-      off = p.ws.grp[g].off;
-      const int items = p.Hkv * p.ws.grp[g].npairs;
-      n = items * p.ws.grp[g].nt;
+      const int off = p.ws.grp[g].off, items = p.Hkv * p.ws.grp[g].npairs;
+      const int n = items * p.ws.grp[g].nt;
       if (n > 0) {
         cf = off / share;
-        rows = ((off + n - 1) / share - cf + items) * p.ws.grp[g].rows;
-        for (int c = (off + share - 1) / share; c * share < off + n; ++c) p.ws.cta[c] = g;
+        rows.x = ((off + n - 1) / share - cf + items) * p.ws.grp[g].rows;
       }
     }
-    const int base = carry + cta_scan(rows, wsum, total);
+    const int2 base = add2(carry, cta_scan(rows, wsum, total));
     if (g < p.n_groups) {
-      p.ws.grp[g].base = base;
+      p.ws.grp[g].base = base.x;
       p.ws.grp[g].cf = cf;
     }
-    carry += total;
+    carry = add2(carry, total);
+  }
+  // the item that every CTA starts in: of a group by a warp, of a row by a thread
+  for (int g = warp; g < p.n_groups; g += kPlan / 32) {
+    const int off = p.ws.grp[g].off, n = p.Hkv * p.ws.grp[g].npairs * p.ws.grp[g].nt;
+    for (int c = (off + share - 1) / share + lane; c * share < off + n; c += 32)
+      p.ws.cta[c].item = g;
   }
   for (int b = threadIdx.x; b < p.B; b += kPlan) {
-    const int off = p.ws.row[b].off, n = p.ws.row[b].nt * p.Hkv;
-    for (int c = (off + share - 1) / share; c * share < off + n; ++c) p.ws.cta[c] = p.n_groups + b;
+    const int off = prefix_units + p.ws.row[b].off, n = p.ws.row[b].nt * p.Hkv;
+    for (int c = (off + share - 1) / share; c * share < off + n; ++c)
+      p.ws.cta[c].item = p.n_groups + b;
   }
-  if (threadIdx.x == 0) *p.ws.head = Head{prefix_units, units, share, carry};
+  if (threadIdx.x == 0) *p.ws.head = Head{share, carry.x};
 }
 
 // ---------------------------------------------------------------------------- attend
@@ -269,6 +276,7 @@ struct Misc {
   uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
   uint64_t seg_full[NSEG], seg_empty[NSEG], fin;
   Seg seg[NSEG];
+  int left[NSEG][2], both[NSEG];   // the MMA warp's: Q K^T to come, streams done
   int2 nv[NSLOT];       // of a V slot: valid keys of the tile's two 64-key halves
   uint32_t tmem_base;
   int abort_flag;
@@ -515,17 +523,26 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
   if (warp == 8) {
     // ------------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      const Head hd = *p.ws.head;
-      const int a = blockIdx.x * hd.share, e = min(a + hd.share, hd.units);
+      const CtaRec me = p.ws.cta[blockIdx.x];
+      const int suffix_base = p.ws.head->suffix_base;
+      const int e = me.e;
+      int pos = me.a, at = me.item;
       bool ok = true;
       int nseg = 0, slots = 0;                   // segments begun, K/V slots loaded so far
       int qn[2] = {0, 0};                        // loads of each query slot so far
-      int at = a < e ? p.ws.cta[blockIdx.x] : 0;
-      int pos = a;
+      // The row being read by itself and the one after it: record, length and the pages
+      // of its first tile, asked for a row ahead (a row can be one tile for each KV head).
+      auto clamped = [&](int len) { return min(max(len, 0), p.NB * p.blk); };
+      auto page_of = [&](int row, int key, int end) -> int {
+        return key < end ? p.table[(size_t)row * p.NB + key / p.blk] : -2;
+      };
+      RowRec r = {}, nr = {};
+      int len = 0, nlen = 0, pgA = -2, pgB = -2, npgA = -2, npgB = -2, b = -1;
+      bool npg = false;
       while (ok) {
         Seg s = {};
-        int key0 = 0, key_end = 0, trow = 0, mrows = 0;
-        while (pos < e && pos < hd.prefix_units) {
+        int key0 = 0, key_end = 0, trow = 0, mrows = 0, pg0 = -2, pg1 = -2;
+        while (pos < e && pos < me.prefix_units) {
           const GroupRec g = p.ws.grp[at];
           const int items = p.Hkv * g.npairs, local = pos - g.off;
           if (g.nt == 0 || local >= items * g.nt) {
@@ -549,31 +566,55 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
           key_end = g.nb * p.blk;
           trow = g.leader;
           mrows = TILE;
+          pg0 = page_of(trow, key0, key_end);
+          pg1 = page_of(trow, key0 + SUB, key_end);
           break;
         }
         if (!s.live && pos < e) {
-          int b = at - p.n_groups;
+          const int own = pos - me.prefix_units;
           if (b < 0) {
-            b = 0;
-            at = p.n_groups;
+            b = max(at - p.n_groups, 0);
+            r = p.ws.row[b];
+            len = clamped(p.lengths[b]);
+            if (b + 1 < p.B) {
+              nr = p.ws.row[b + 1];
+              nlen = p.lengths[b + 1];
+            }
+            pgA = page_of(b, r.start * p.blk, len);
+            pgB = page_of(b, r.start * p.blk + SUB, len);
           }
-          while (b < p.B && pos >= p.ws.row[b].off + p.ws.row[b].nt * p.Hkv) ++b;
-          at = p.n_groups + b;
+          while (b < p.B && own >= r.off + r.nt * p.Hkv) {
+            if (!npg && b + 1 < p.B) {
+              npgA = page_of(b + 1, nr.start * p.blk, clamped(nlen));
+              npgB = page_of(b + 1, nr.start * p.blk + SUB, clamped(nlen));
+            }
+            ++b;
+            r = nr;
+            len = clamped(nlen);
+            pgA = npgA;
+            pgB = npgB;
+            npg = false;
+            if (b + 1 < p.B) {
+              nr = p.ws.row[b + 1];
+              nlen = p.lengths[b + 1];
+            }
+          }
           if (b < p.B) {
-            const RowRec r = p.ws.row[b];
-            const int local = pos - r.off, g = local / r.nt, t = local - g * r.nt;
+            const int local = own - r.off, g = local / r.nt, t = local - g * r.nt;
             s.live = 1;
             s.pair = 0;
             s.ntiles = min(r.nt - t, e - pos);
             s.row0 = b;
             s.kvh = g;
             s.mA = s.mB = p.G;
-            s.partA = hd.suffix_base + ((int)blockIdx.x + b * p.Hkv + g) * 2 * p.G;
+            s.partA = suffix_base + ((int)blockIdx.x + b * p.Hkv + g) * 2 * p.G;
             s.partB = s.partA + p.G;
             key0 = r.start * p.blk + t * TILE;
-            key_end = min(max(p.lengths[b], 0), p.NB * p.blk);
+            key_end = len;
             trow = b;
             mrows = p.G;
+            pg0 = t == 0 ? pgA : page_of(b, key0, len);
+            pg1 = t == 0 ? pgB : page_of(b, key0 + SUB, len);
           }
         }
         s.base = slots / 2;
@@ -588,17 +629,12 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
         ms->seg[sl] = s;
         mbar_arrive(&ms->seg_full[sl]);
         if (!s.live) break;
-        const int* trow_p = p.table + (size_t)trow * p.NB;
-        auto page_at = [&](int key) -> int {
-          return key < key_end ? trow_p[key / p.blk] : -2;
-        };
-        int pg0 = page_at(key0), pg1 = page_at(key0 + SUB);
         for (int t = 0; t < s.ntiles && ok; ++t) {
           const int k0 = key0 + t * TILE;
           const int pg[2] = {pg0, pg1};
           if (t + 1 < s.ntiles) {
-            pg0 = page_at(k0 + TILE);
-            pg1 = page_at(k0 + TILE + SUB);
+            pg0 = page_of(trow, k0 + TILE, key_end);
+            pg1 = page_of(trow, k0 + TILE + SUB, key_end);
           }
           int nv[2] = {max(min(key_end - k0, SUB), 0), max(min(key_end - k0 - SUB, SUB), 0)};
 #pragma unroll
@@ -650,6 +686,11 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
         }
         pos += s.ntiles;
         ++nseg;
+        if (b >= 0 && !npg && b + 1 < p.B) {     // the next row's record is here by now
+          npgA = page_of(b + 1, nr.start * p.blk, clamped(nlen));
+          npgB = page_of(b + 1, nr.start * p.blk + SUB, clamped(nlen));
+          npg = true;
+        }
       }
       if (!ok) {
         // wait (bounded) for every copy this thread issued before the CTA exits
@@ -671,10 +712,7 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
       int nseg[2] = {0, 0}, jobs[2] = {0, 0};    // the stream's segment, and its jobs there
       int qk[2] = {0, 0}, pv[2] = {0, 0};        // of which issued
       int cnt[2] = {0, 0}, used[2] = {0, 0};     // jobs, and segments with jobs, before it
-      int left[NSEG][2], both[NSEG];             // per segment: Q K^T to come, streams done
       bool open[2] = {false, false}, over[2] = {false, false};
-#pragma unroll
-      for (int r = 0; r < NSEG; ++r) left[r][0] = left[r][1] = both[r] = 0;
       const uint32_t q0 = smem_u32(smem + C::OFF_Q), kv0 = smem_u32(smem + C::OFF_KV);
       bool ok = true;
       uint32_t idle = 0;
@@ -697,13 +735,8 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
             open[x] = true;
             if (nseg[x ^ 1] <= nseg[x] && !(open[x ^ 1] && nseg[x ^ 1] == nseg[x])) {
               // the first of the two streams to get here
-#pragma unroll
-              for (int r = 0; r < NSEG; ++r)
-                if (r == sl) {
-                  left[r][0] = s[x].pair ? s[x].ntiles : s[x].flip == 0 ? s[x].ntiles : 0;
-                  left[r][1] = s[x].pair ? s[x].ntiles : s[x].flip == 1 ? s[x].ntiles : 0;
-                  both[r] = 0;
-                }
+              ms->left[sl][0] = ms->left[sl][1] = s[x].ntiles;
+              ms->both[sl] = 0;
             }
           }
           const int sl = nseg[x] % NSEG;
@@ -754,11 +787,7 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
               if (!s[x].pair || nseg[x ^ 1] > nseg[x] ||
                   (open[x ^ 1] && nseg[x ^ 1] == nseg[x] && qk[x ^ 1] > tile))
                 mma_commit(&ms->kv_empty[C::kslot(T)]);
-#pragma unroll
-              for (int r = 0; r < NSEG; ++r)
-#pragma unroll
-                for (int y = 0; y < 2; ++y)
-                  if (r == sl && y == qs && --left[r][y] == 0) mma_commit(&ms->q_empty[y]);
+              if (--ms->left[sl][qs] == 0) mma_commit(&ms->q_empty[qs]);
               did = true;
             }
           }
@@ -767,9 +796,7 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
             used[x] += jobs[x] > 0;
             ++nseg[x];
             open[x] = false;
-#pragma unroll
-            for (int r = 0; r < NSEG; ++r)
-              if (r == sl && ++both[r] == 2) mbar_arrive(&ms->seg_empty[r]);
+            if (++ms->both[sl] == 2) mbar_arrive(&ms->seg_empty[sl]);
             did = true;
           }
         }
@@ -999,25 +1026,33 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
 constexpr int kCombine = 512;
 constexpr int kMaxSlots = 1024;
 
-// One CTA per (row, head): thread = (slot group, dim).  The slots are the CTAs that had a
-// piece of the row's prefix item (one or two streams each) and of its own item.
-template <int D, typename OutT>
+ETA_DEV void store4(float* o, float4 v) { *reinterpret_cast<float4*>(o) = v; }
+ETA_DEV void store4(__nv_bfloat16* o, float4 v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                            *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// One CTA per (row, KV head), its G heads together (their partial rows lie side by side).
+// The slots are the CTAs that had a piece of the row's prefix item (one or two streams
+// each) and of its own item.  Thread = (slot group, 4 dims of a head).
+template <int D, int G, typename OutT>
 __global__ void __launch_bounds__(kCombine)
 shared_combine_kernel(const AttendParams p, OutT* __restrict__ o, float* __restrict__ lse) {
   ETA_PDL_ENTRY();
-  constexpr int NG = kCombine / D;
-  __shared__ int slot[kMaxSlots];
-  __shared__ float w[kMaxSlots];
-  __shared__ float red[kCombine / 32], acc[NG][D];
-  const int b = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq, kvh = h / p.G, hg = h % p.G;
+  constexpr int VEC = G * D / 4, NG = kCombine / VEC, NW = kCombine / 32;
+  __shared__ float w[kMaxSlots * G];
+  __shared__ float red[NW][G];
+  __shared__ float4 acc[kCombine];
+  const int b = blockIdx.x / p.Hkv, kvh = blockIdx.x % p.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Head hd = *p.ws.head;
   const RowRec r = p.ws.row[b];
   int n1 = 0, first1 = 0, step1 = 0, two1 = 0, off1 = 0;    // prefix slots
   if (r.group >= 0) {
     const GroupRec g = p.ws.grp[r.group];
-    const int i = (b - g.row0) * p.G + hg, pair = i / (2 * TILE), ii = i % (2 * TILE);
-    const int item = kvh * g.npairs + pair, left = g.nrows * p.G - pair * 2 * TILE;
+    const int i = (b - g.row0) * G, pair = i / (2 * TILE), ii = i % (2 * TILE);
+    const int item = kvh * g.npairs + pair, left = g.nrows * G - pair * 2 * TILE;
     const int a = g.off + item * g.nt, c0 = a / hd.share;
     n1 = (a + g.nt - 1) / hd.share - c0 + 1;
     first1 = g.base + (c0 - g.cf + item) * g.rows + ii;
@@ -1027,52 +1062,94 @@ shared_combine_kernel(const AttendParams p, OutT* __restrict__ o, float* __restr
   }
   int n2 = 0, first2 = 0;                                   // the row's own slots
   if (r.nt > 0) {
-    const int a = r.off + kvh * r.nt, c0 = a / hd.share;
+    const int a = p.ws.cta[0].prefix_units + r.off + kvh * r.nt, c0 = a / hd.share;
     n2 = (a + r.nt - 1) / hd.share - c0 + 1;
-    first2 = hd.suffix_base + (c0 + b * p.Hkv + kvh) * 2 * p.G + hg;
+    first2 = hd.suffix_base + (c0 + b * p.Hkv + kvh) * 2 * G;
   }
   const int m1 = n1 * (1 + two1), n = min(m1 + 2 * n2, kMaxSlots);
-  float mx = -INFINITY;
-  for (int k = tid; k < n; k += kCombine) {
+  auto slot = [&](int k) -> int {          // partial row of slot k's first head
     int s;
     if (k < m1) s = two1 ? first1 + (k >> 1) * step1 + (k & 1) * off1 : first1 + k * step1;
-    else s = first2 + ((k - m1) >> 1) * 2 * p.G + ((k - m1) & 1) * p.G;
-    if (!ETA_IN_BOUNDS(s, p.part_rows, p.status)) s = 0;
-    slot[k] = s;
-    const float v = p.ws.part_ml[2 * (size_t)s];
-    w[k] = v;
-    mx = fmaxf(mx, v);
-  }
-  mx = warp_max(mx);
-  if (lane == 0) red[warp] = mx;
-  __syncthreads();
-  mx = red[0];
+    else s = first2 + (k - m1) * G;
+    return ETA_RANGE_IN_BOUNDS(s, s + G, p.part_rows, p.status) ? s : 0;
+  };
+  // a thread's elements (slot, head) all have the head tid % G
+  auto over_threads = [&](float v, auto op) -> float {
 #pragma unroll
-  for (int i = 1; i < kCombine / 32; ++i) mx = fmaxf(mx, red[i]);
-  __syncthreads();
+    for (int x = 16; x >= G; x >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, x));
+    if (lane < G) red[warp][lane] = v;
+    __syncthreads();
+    v = red[0][tid % G];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) v = op(v, red[i][tid % G]);
+    __syncthreads();
+    return v;
+  };
+  const float2* ml = reinterpret_cast<const float2*>(p.ws.part_ml);
+  constexpr int KEEP = 4;                   // elements a thread keeps (512 slots of 4 heads)
+  float2 kept[KEEP];
+  float mx = -INFINITY;
+#pragma unroll
+  for (int u = 0; u < KEEP; ++u) {
+    const int x = tid + u * kCombine;
+    kept[u] = x < n * G ? ml[slot(x / G) + x % G] : make_float2(-INFINITY, 0.f);
+    mx = fmaxf(mx, kept[u].x);
+  }
+  for (int x = tid + KEEP * kCombine; x < n * G; x += kCombine)
+    mx = fmaxf(mx, ml[slot(x / G) + x % G].x);
+  mx = over_threads(mx, [](float a, float c) { return fmaxf(a, c); });
   float l = 0.f;
-  for (int k = tid; k < n; k += kCombine) {
-    const float e = mx == -INFINITY ? 0.f : expf(w[k] - mx);
-    w[k] = e;
-    l = fmaf(e, p.ws.part_ml[2 * (size_t)slot[k] + 1], l);
-  }
-  l = warp_sum(l);
-  if (lane == 0) red[warp] = l;
-  __syncthreads();
-  l = 0.f;
+  auto weigh = [&](int x, float2 v) {
+    const float e = mx == -INFINITY ? 0.f : expf(v.x - mx);
+    w[x] = e;
+    l = fmaf(e, v.y, l);
+  };
 #pragma unroll
-  for (int i = 0; i < kCombine / 32; ++i) l += red[i];
-  const int dd = tid % D, gi = tid / D;
-  float a = 0.f;
-#pragma unroll 4
-  for (int k = gi; k < n; k += NG)
-    if (w[k] > 0.f) a = fmaf(w[k], p.ws.part_o[(size_t)slot[k] * D + dd], a);
-  acc[gi][dd] = a;
+  for (int u = 0; u < KEEP; ++u)
+    if (tid + u * kCombine < n * G) weigh(tid + u * kCombine, kept[u]);
+  for (int x = tid + KEEP * kCombine; x < n * G; x += kCombine)
+    weigh(x, ml[slot(x / G) + x % G]);
+  l = over_threads(l, [](float a, float c) { return a + c; });
+  const size_t head0 = (size_t)b * p.Hq + kvh * G;
+  if (tid < G) {
+    lse[head0 + tid] = l > 0.f ? mx + logf(l) : -INFINITY;
+    red[0][tid] = l;
+  }
+  const int v = tid % VEC, gi = tid / VEC, h = v / (D / 4);
+  const float4* po = reinterpret_cast<const float4*>(p.ws.part_o);
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int k = gi; k < n; k += NG) {
+    const float4 x = po[(size_t)slot(k) * (D / 4) + v];
+    const float e = w[k * G + h];
+    if (e > 0.f) {                          // an empty slot's o was never written
+      a.x = fmaf(e, x.x, a.x);
+      a.y = fmaf(e, x.y, a.y);
+      a.z = fmaf(e, x.z, a.z);
+      a.w = fmaf(e, x.w, a.w);
+    }
+  }
+  acc[tid] = a;
   __syncthreads();
   if (gi == 0) {
 #pragma unroll
-    for (int i = 1; i < NG; ++i) a += acc[i][dd];
-    combine_store<D>(o, lse, (size_t)b * p.Hq + h, dd, mx, l, a);
+    for (int i = 1; i < NG; ++i) {
+      const float4 y = acc[i * VEC + v];
+      a.x += y.x;
+      a.y += y.y;
+      a.z += y.z;
+      a.w += y.w;
+    }
+    const float L = red[0][h];
+    if (L > 0.f) {
+      a.x /= L;
+      a.y /= L;
+      a.z /= L;
+      a.w /= L;
+    } else {
+      a = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    store4(o + head0 * D + v * 4, a);
   }
 }
 
@@ -1092,7 +1169,7 @@ inline WsOff ws_off(const eta_dims_t* d, int n_groups, int P) {
   w.head = x; x += 256;
   w.grp = x;  x = align_up(x + (size_t)n_groups * sizeof(GroupRec), 256);
   w.row = x;  x = align_up(x + (size_t)d->B * sizeof(RowRec), 256);
-  w.cta = x;  x = align_up(x + (size_t)P * 4, 256);
+  w.cta = x;  x = align_up(x + (size_t)P * sizeof(CtaRec), 256);
   w.ml = x;   x = align_up(x + rows * 8, 256);
   w.o = x;    x = align_up(x + rows * d->d * 4, 256);
   w.total = x;
@@ -1132,6 +1209,21 @@ eta_status_t launch_attend_d(int gate, bool two, const CUtensorMap& mq, const CU
     case 4: return launch_attend<D, SOFT, 1>(mq, mq1, mk, mv, a, P, s);
     default: return launch_attend<D, SOFT, 2>(mq, mq1, mk, mv, a, P, s);
   }
+}
+
+template <int G>
+eta_status_t launch_combine(const eta_dims_t* d, bool f32, const AttendParams& a, void* o,
+                            float* lse, cudaStream_t s) {
+  const dim3 grid(d->B * d->Hkv), block(kCombine);
+  if (f32)
+    return d->d == 64 ? launch_k(shared_combine_kernel<64, G, float>, grid, block, 0, s, a,
+                                 static_cast<float*>(o), lse)
+                      : launch_k(shared_combine_kernel<128, G, float>, grid, block, 0, s, a,
+                                 static_cast<float*>(o), lse);
+  return d->d == 64 ? launch_k(shared_combine_kernel<64, G, __nv_bfloat16>, grid, block, 0, s, a,
+                               static_cast<__nv_bfloat16*>(o), lse)
+                    : launch_k(shared_combine_kernel<128, G, __nv_bfloat16>, grid, block, 0, s, a,
+                               static_cast<__nv_bfloat16*>(o), lse);
 }
 
 // q [B, Hq, d] as (dim, head, row); box 64 x G x rows, 128-byte swizzle.
@@ -1196,7 +1288,7 @@ extern "C" eta_status_t eta_shared_decode(const eta_dims_t* dims, int32_t n_page
   wp.head = reinterpret_cast<sd::Head*>(w + L.head);
   wp.grp = reinterpret_cast<sd::GroupRec*>(w + L.grp);
   wp.row = reinterpret_cast<sd::RowRec*>(w + L.row);
-  wp.cta = reinterpret_cast<int32_t*>(w + L.cta);
+  wp.cta = reinterpret_cast<sd::CtaRec*>(w + L.cta);
   wp.part_ml = reinterpret_cast<float*>(w + L.ml);
   wp.part_o = reinterpret_cast<float*>(w + L.o);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1220,14 +1312,10 @@ extern "C" eta_status_t eta_shared_decode(const eta_dims_t* dims, int32_t n_page
            : sd::launch_attend_d<128>(gate, two, mq, mq1, mk, mv, a, P, s);
   if (st != ETA_OK) return st;
 
-  const dim3 grid(dims->B * dims->Hq), block(sd::kCombine);
-  if (two)
-    return d64 ? launch_k(sd::shared_combine_kernel<64, float>, grid, block, 0, s, a,
-                          static_cast<float*>(o), lse)
-               : launch_k(sd::shared_combine_kernel<128, float>, grid, block, 0, s, a,
-                          static_cast<float*>(o), lse);
-  return d64 ? launch_k(sd::shared_combine_kernel<64, __nv_bfloat16>, grid, block, 0, s, a,
-                        static_cast<__nv_bfloat16*>(o), lse)
-             : launch_k(sd::shared_combine_kernel<128, __nv_bfloat16>, grid, block, 0, s, a,
-                        static_cast<__nv_bfloat16*>(o), lse);
+  switch (G) {
+    case 1: return sd::launch_combine<1>(dims, two, a, o, lse, s);
+    case 2: return sd::launch_combine<2>(dims, two, a, o, lse, s);
+    case 4: return sd::launch_combine<4>(dims, two, a, o, lse, s);
+    default: return sd::launch_combine<8>(dims, two, a, o, lse, s);
+  }
 }
