@@ -11,12 +11,12 @@
 // bound by the tensor cores and the exponentials from about 256 (row, head) pairs on.
 //
 // Three launches:
-//   shared_plan_kernel   (one CTA) the work list.  A unit is a 128-key tile of an item; an
-//                        item is (group, KV head, up to 256 (row, head) pairs) over the
-//                        prefix, or (row, KV head) over the row's own keys.  All units,
-//                        laid end to end, are cut into equal shares, one per SM.
-//   shared_attend_kernel one CTA per share: 320 threads, warps 0-3 / 4-7 the softmax of
-//                        streams A / B, warp 8 the TMA producer, warp 9 the MMA issuer.
+//   shared_plan_kernel   (one CTA) the work list.  An item is (group, KV head, up to 256
+//                        (row, head) pairs) over the prefix, or (row, KV head) over the
+//                        row's own keys, in key tiles of 128.  The items' costs, laid end
+//                        to end, are cut into equal shares, one per SM.
+//   shared_attend_kernel one CTA per share: 352 threads, warps 0-3 / 4-7 the softmax of
+//                        streams A / B, warp 8 the TMA producer, warps 9 / 10 their MMAs.
 //                        S_x = Q K^T and O_x += P V with M = 128 queries, N = 128 keys;
 //                        a thread owns a query row, so no row statistic is exchanged.
 //                        Two streams keep the tensor cores busy while the other stream's
@@ -52,30 +52,41 @@ constexpr int TILE = 128;                       // query rows and keys of a tile
 constexpr int SUB = 64;                         // keys of a TMA box (half a tile)
 constexpr int HALF = TILE * 128;                // [128 rows x 64 dims] bf16 = 16 KB
 constexpr int NSEG = 4;                         // segment records in flight
-constexpr int NT = 320;
+constexpr int NT = 352;
 constexpr int kPlan = 1024;
 constexpr int kTmemCols = 512;
-constexpr uint32_t kIdleLimit = 1u << 24;       // polls of the MMA warp without an event
+constexpr uint32_t kIssueLimit = 1u << 26;      // polls for a load to be issued
 constexpr float kRescale = 8.0f;                // rescale O when the max grows by > 8 (e^8)
 constexpr float kLog2e = 1.4426950408889634f;
 enum Gate { NONE = 0, HARD = 1, SOFT = 2 };
 
 // ------------------------------------------------------------------------- work list
+// Costs in half microseconds, as measured (64 rows over 128K tokens, 4 KV heads): a key
+// tile of up to 256 or 128 queries, a key tile of a row's own, and what a row's own item
+// costs besides (its few tiles cannot fill the pipeline).  An item's tiles begin at 0 and
+// kSegCost + t * cost; a CTA has the tiles that begin in its share of the costs.
+constexpr int kPairCost = 4, kSingleCost = 3, kOwnCost = 3, kSegCost = 4;
+constexpr int kMinShare = kOwnCost + kSegCost;  // every share inside an item has a tile's begin
+static_assert(kMinShare >= kPairCost && kMinShare >= kSingleCost, "smallest share");
+ETA_DEV int own_begin(int t) { return t ? kSegCost + t * kOwnCost : 0; }
+ETA_DEV int own_cost(int nt) { return nt ? kSegCost + nt * kOwnCost : 0; }
+
 struct GroupRec {
-  int off;        // first unit
-  int nt;         // units (key tiles) of an item; 0: nothing is shared
+  int off;        // its first item's place in the costs
+  int nt;         // key tiles of an item; 0: nothing is shared
+  int cost;       // of a key tile
   int npairs;     // 256-row items per KV head
   int row0, nrows;
   int leader;     // the row whose table names the prefix pages
   int nb;         // shared blocks
   int rows;       // partial rows of a slot
   int base;       // first partial row of the group's slots
-  int cf;         // CTA of its first unit
+  int cf;         // CTA of its first tile
 };
 
 struct RowRec {
-  int off;        // first unit, counted behind all prefix units
-  int nt;         // units per KV head
+  int off;        // its first item's place, counted behind all prefixes
+  int nt;         // key tiles per KV head
   int start;      // first block that the row reads by itself
   int group;      // the group it shares a prefix with, or -1
 };
@@ -84,10 +95,10 @@ struct Head {
   int share, suffix_base;
 };
 
-// What a CTA begins with: its units [a, e), the item of unit a (the group, or n_groups +
-// row), and where the rows' own units begin.
+// What a CTA begins with: its share [a, e) of the costs, the group (or n_groups + row) at
+// a, and the cost of all prefixes.
 struct CtaRec {
-  int a, e, item, prefix_units;
+  int a, e, item, prefix_cost;
 };
 
 struct Ws {
@@ -179,6 +190,7 @@ __global__ void __launch_bounds__(kPlan) shared_plan_kernel(const PlanParams p) 
       GroupRec rec;
       const int rows = (r1 - r0) * p.G;
       rec.nt = share ? (nb * p.blk + TILE - 1) / TILE : 0;
+      rec.cost = rows > TILE ? kPairCost : kSingleCost;
       rec.npairs = (rows + 2 * TILE - 1) / (2 * TILE);
       rec.row0 = r0;
       rec.nrows = r1 - r0;
@@ -190,29 +202,32 @@ __global__ void __launch_bounds__(kPlan) shared_plan_kernel(const PlanParams p) 
     }
   }
   __syncthreads();
-  // first units: of the groups (x) and of the rows (y, counted from zero)
+  // places in the costs: of the groups (x) and of the rows (y, counted from zero)
   int2 carry = make_int2(0, 0), total;
   for (int i0 = 0; i0 < max(p.n_groups, p.B); i0 += kPlan) {
     const int i = i0 + threadIdx.x;
     int2 n = make_int2(0, 0);
-    if (i < p.n_groups) n.x = p.Hkv * p.ws.grp[i].npairs * p.ws.grp[i].nt;
+    if (i < p.n_groups) {
+      const GroupRec g = p.ws.grp[i];
+      n.x = p.Hkv * g.npairs * g.nt * g.cost;
+    }
     if (i < p.B) {
       const int len = min(max(p.lengths[i], 0), cap);
       const int nt = (max(len - p.ws.row[i].start * p.blk, 0) + TILE - 1) / TILE;
       p.ws.row[i].nt = nt;
-      n.y = p.Hkv * nt;
+      n.y = p.Hkv * own_cost(nt);
     }
     const int2 off = add2(carry, cta_scan(n, wsum, total));
     if (i < p.n_groups) p.ws.grp[i].off = off.x;
     if (i < p.B) p.ws.row[i].off = off.y;
     carry = add2(carry, total);
   }
-  const int prefix_units = carry.x, units = carry.x + carry.y;
-  const int share = max((units + p.P - 1) / p.P, 1);
+  const int prefix_cost = carry.x, costs = carry.x + carry.y;
+  const int share = max((costs + p.P - 1) / p.P, kMinShare);
   for (int c = threadIdx.x; c < p.P; c += kPlan) {
-    p.ws.cta[c].a = min(c * share, units);
-    p.ws.cta[c].e = min(c * share + share, units);
-    p.ws.cta[c].prefix_units = prefix_units;
+    p.ws.cta[c].a = min(c * share, costs);
+    p.ws.cta[c].e = min(c * share + share, costs);
+    p.ws.cta[c].prefix_cost = prefix_cost;
   }
   // where a group's partial results go
   carry = make_int2(0, 0);
@@ -222,7 +237,7 @@ __global__ void __launch_bounds__(kPlan) shared_plan_kernel(const PlanParams p) 
     int cf = 0;
     if (g < p.n_groups) {
       const int off = p.ws.grp[g].off, items = p.Hkv * p.ws.grp[g].npairs;
-      const int n = items * p.ws.grp[g].nt;
+      const int n = items * p.ws.grp[g].nt * p.ws.grp[g].cost;
       if (n > 0) {
         cf = off / share;
         rows.x = ((off + n - 1) / share - cf + items) * p.ws.grp[g].rows;
@@ -237,12 +252,13 @@ __global__ void __launch_bounds__(kPlan) shared_plan_kernel(const PlanParams p) 
   }
   // the item that every CTA starts in: of a group by a warp, of a row by a thread
   for (int g = warp; g < p.n_groups; g += kPlan / 32) {
-    const int off = p.ws.grp[g].off, n = p.Hkv * p.ws.grp[g].npairs * p.ws.grp[g].nt;
+    const GroupRec r = p.ws.grp[g];
+    const int off = r.off, n = p.Hkv * r.npairs * r.nt * r.cost;
     for (int c = (off + share - 1) / share + lane; c * share < off + n; c += 32)
       p.ws.cta[c].item = g;
   }
   for (int b = threadIdx.x; b < p.B; b += kPlan) {
-    const int off = prefix_units + p.ws.row[b].off, n = p.ws.row[b].nt * p.Hkv;
+    const int off = prefix_cost + p.ws.row[b].off, n = p.Hkv * own_cost(p.ws.row[b].nt);
     for (int c = (off + share - 1) / share; c * share < off + n; ++c)
       p.ws.cta[c].item = p.n_groups + b;
   }
@@ -259,8 +275,9 @@ struct Seg {
   int mA, mB;           // valid query rows of the streams' tiles
   int partA, partB;     // first partial row of each stream
   int check;            // prefix: rows that do not share it are left out
-  int flip;             // single: the stream of the first key tile, and the query slot
-  int qph;              // bit s: the phase of query slot s that holds the segment's queries
+  int flip;             // single: the stream of the first key tile
+  int qslot;            // single: the query slot
+  int qn[2];            // loads of each query slot before the segment's
 };
 
 // Jobs (key tiles) of stream x in a segment, and the tile of job j.
@@ -273,11 +290,11 @@ template <int D>
 struct Misc {
   static constexpr int NSLOT = D == 128 ? 5 : 10;
   uint64_t q_full[2], q_empty[2], kv_full[NSLOT], kv_empty[NSLOT];
-  uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
-  uint64_t seg_full[NSEG], seg_empty[NSEG], fin;
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], o_free[2];   // [stream][half tile]
+  uint64_t seg_full[NSEG], seg_empty[NSEG], fin[2];
   Seg seg[NSEG];
-  int left[NSEG][2], both[NSEG];   // the MMA warp's: Q K^T to come, streams done
   int2 nv[NSLOT];       // of a V slot: valid keys of the tile's two 64-key halves
+  int issued, q_issued[2];   // K and V tiles, and queries of each slot, under way so far
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -295,9 +312,9 @@ struct Cfg {
   static constexpr int OFF_MISC = OFF_KV + NSLOT * SLOT;
   static constexpr int SMEM = OFF_MISC + (int)sizeof(Misc<D>) + 1024;
   ETA_DEV static int kslot(int t) { return 2 * t % NSLOT; }
-  ETA_DEV static uint32_t kphase(int t) { return (uint32_t)(2 * t / NSLOT) & 1u; }
+  ETA_DEV static int kload(int t) { return 2 * t / NSLOT; }
   ETA_DEV static int vslot(int t) { return (2 * t + 1) % NSLOT; }
-  ETA_DEV static uint32_t vphase(int t) { return (uint32_t)((2 * t + 1) / NSLOT) & 1u; }
+  ETA_DEV static int vload(int t) { return (2 * t + 1) / NSLOT; }
 };
 static_assert(Cfg<128>::SMEM <= 227 * 1024, "shared decode shared memory");
 
@@ -353,16 +370,6 @@ ETA_DEV void tmem_st32(uint32_t taddr, const uint32_t* v) {
       : "memory");
 }
 
-ETA_DEV void tmem_st16(uint32_t taddr, const uint32_t* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
-      "r"(v[15])
-      : "memory");
-}
-
 // Waits for the thread's loads; the 32 values are operands so that their use stays behind.
 ETA_DEV void tmem_wait_ld32(float* v) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -402,17 +409,20 @@ ETA_DEV void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
       : "memory");
 }
 
-// Whether phase `parity` of `bar` is over, without waiting.
-ETA_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n"
-      " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
+// Waits for load number n (from 0) of a slot, which is number `item` of those that the
+// producer counts in *issued.  A wait for a phase's parity also ends while the phase before
+// it is open, and a stream does not follow the loads of the other's tiles: so first that
+// the load has been issued (the slot's loads before it are then over), then that it is in.
+ETA_DEV bool wait_issued(volatile int* issued, int item, volatile int* abort) {
+  uint32_t polls = 0;
+  while (*issued <= item)
+    if (++polls > kIssueLimit || *abort) return false;
+  __threadfence_block();
+  return true;
+}
+ETA_DEV bool wait_load(uint64_t* bar, int n, volatile int* issued, int item,
+                       volatile int* abort) {
+  return wait_issued(issued, item, abort) && mbar_wait(bar, (uint32_t)n & 1u, abort);
 }
 
 // The gate on 32 scores of a query row, in raw units (see the softmax).
@@ -489,21 +499,24 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NSLOT; ++s) {
       mbar_init(&ms->kv_full[s], 1);
-      mbar_init(&ms->kv_empty[s], 1);
+      mbar_init(&ms->kv_empty[s], 2);           // both streams, or one of them twice
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&ms->q_full[x], 1);
-      mbar_init(&ms->q_empty[x], 1);
-      mbar_init(&ms->s_full[x], 1);
-      mbar_init(&ms->p_full[x], 4);
-      mbar_init(&ms->pv_done[x], 1);
+      mbar_init(&ms->q_empty[x], 2);
+      mbar_init(&ms->fin[x], 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&ms->s_full[x][h], 1);
+        mbar_init(&ms->p_full[x][h], 4);
+        mbar_init(&ms->pv_done[x][h], 1);
+      }
       mbar_init(&ms->o_free[x], 4);
     }
     for (int s = 0; s < NSEG; ++s) {
       mbar_init(&ms->seg_full[s], 1);
-      mbar_init(&ms->seg_empty[s], 9);          // 8 softmax warps and the MMA warp
+      mbar_init(&ms->seg_empty[s], 10);         // 8 softmax warps and the MMA warps
     }
-    mbar_init(&ms->fin, 1);
+    ms->issued = ms->q_issued[0] = ms->q_issued[1] = 0;
     ms->abort_flag = 0;
     fence_mbar_init();
   }
@@ -522,296 +535,354 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
 
   if (warp == 8) {
     // ------------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      const CtaRec me = p.ws.cta[blockIdx.x];
-      const int suffix_base = p.ws.head->suffix_base;
-      const int e = me.e;
-      int pos = me.a, at = me.item;
-      bool ok = true;
-      int nseg = 0, slots = 0;                   // segments begun, K/V slots loaded so far
-      int qn[2] = {0, 0};                        // loads of each query slot so far
-      // The row being read by itself and the one after it: record, length and the pages
-      // of its first tile, asked for a row ahead (a row can be one tile for each KV head).
-      auto clamped = [&](int len) { return min(max(len, 0), p.NB * p.blk); };
-      auto page_of = [&](int row, int key, int end) -> int {
-        return key < end ? p.table[(size_t)row * p.NB + key / p.blk] : -2;
-      };
-      RowRec r = {}, nr = {};
-      int len = 0, nlen = 0, pgA = -2, pgB = -2, npgA = -2, npgB = -2, b = -1;
-      bool npg = false;
-      while (ok) {
-        Seg s = {};
-        int key0 = 0, key_end = 0, trow = 0, mrows = 0, pg0 = -2, pg1 = -2;
-        while (pos < e && pos < me.prefix_units) {
-          const GroupRec g = p.ws.grp[at];
-          const int items = p.Hkv * g.npairs, local = pos - g.off;
-          if (g.nt == 0 || local >= items * g.nt) {
-            if (++at >= p.n_groups) break;       // cannot happen: a unit has an item
-            continue;
+    // The whole warp: 32 pages are looked up at a time, a tile's boxes are issued by a
+    // lane each.  Every variable but the lane's own page and box is the same in all lanes.
+    const CtaRec me = p.ws.cta[blockIdx.x];
+    const int suffix_base = p.ws.head->suffix_base;
+    const int e = me.e, shift = p.blk == 64 ? 6 : 7;
+    int pos = me.a, at = me.item;
+    bool ok = true;
+    int nseg = 0, slots = 0;                     // segments begun, K/V slots loaded so far
+    int qn[2] = {0, 0};                          // loads of each query slot so far
+    // The lane's 64-key piece of a row: piece k0 / 64 + lane; its page, or -2 past the end.
+    auto page_of = [&](int row, int k0, int end) -> int {
+      const int key = k0 + lane * SUB;
+      return key < end ? p.table[(size_t)row * p.NB + (key >> shift)] : -2;
+    };
+    auto clamped = [&](int len) { return min(max(len, 0), p.NB << shift); };
+    // The row being read by itself and the one after it: record, length and first pages,
+    // asked for a row ahead (a row can be one tile for each KV head).
+    RowRec r = {}, nr = {};
+    int len = 0, nlen = 0, pg_row = -2, npg_row = -2, b = -1;
+    bool npg = false;
+    auto next_row = [&] {
+      if (b + 1 < p.B) {
+        nr = p.ws.row[b + 1];
+        nlen = p.lengths[b + 1];
+      }
+    };
+    auto next_pages = [&] {
+      if (!npg && b + 1 < p.B) npg_row = page_of(b + 1, nr.start << shift, clamped(nlen));
+      npg = true;
+    };
+    // every lane polls; all agree on the outcome
+    auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+    };
+    while (ok) {
+      Seg s = {};
+      int key0 = 0, key_end = 0, trow = 0, mrows = 0, pg = -2;
+      while (pos < e && pos < me.prefix_cost) {
+        const GroupRec g = p.ws.grp[at];
+        const int items = p.Hkv * g.npairs, ic = g.nt * g.cost, local = pos - g.off;
+        if (ic == 0 || local >= items * ic) {
+          if (++at >= p.n_groups) {              // only when the next place is a row's
+            pos = me.prefix_cost;
+            break;
           }
-          const int item = local / g.nt, t = local - item * g.nt;
-          const int pair = item % g.npairs, i0 = pair * 2 * TILE;
-          const int left = g.nrows * p.G - i0;
-          s.live = 1;
-          s.pair = left > TILE;
-          s.ntiles = min(g.nt - t, e - pos);
-          s.row0 = g.row0 + i0 / p.G;
-          s.kvh = item / g.npairs;
-          s.mA = min(left, TILE);
-          s.mB = s.pair ? min(left - TILE, TILE) : s.mA;
-          s.partA = g.base + ((int)blockIdx.x - g.cf + item) * g.rows;
-          s.partB = s.partA + (!s.pair && g.npairs == 1 ? s.mA : TILE);
-          s.check = 1;
-          key0 = t * TILE;
-          key_end = g.nb * p.blk;
-          trow = g.leader;
-          mrows = TILE;
-          pg0 = page_of(trow, key0, key_end);
-          pg1 = page_of(trow, key0 + SUB, key_end);
-          break;
+          continue;
         }
-        if (!s.live && pos < e) {
-          const int own = pos - me.prefix_units;
-          if (b < 0) {
-            b = max(at - p.n_groups, 0);
-            r = p.ws.row[b];
-            len = clamped(p.lengths[b]);
-            if (b + 1 < p.B) {
-              nr = p.ws.row[b + 1];
-              nlen = p.lengths[b + 1];
-            }
-            pgA = page_of(b, r.start * p.blk, len);
-            pgB = page_of(b, r.start * p.blk + SUB, len);
-          }
-          while (b < p.B && own >= r.off + r.nt * p.Hkv) {
-            if (!npg && b + 1 < p.B) {
-              npgA = page_of(b + 1, nr.start * p.blk, clamped(nlen));
-              npgB = page_of(b + 1, nr.start * p.blk + SUB, clamped(nlen));
-            }
-            ++b;
-            r = nr;
-            len = clamped(nlen);
-            pgA = npgA;
-            pgB = npgB;
-            npg = false;
-            if (b + 1 < p.B) {
-              nr = p.ws.row[b + 1];
-              nlen = p.lengths[b + 1];
-            }
-          }
-          if (b < p.B) {
-            const int local = own - r.off, g = local / r.nt, t = local - g * r.nt;
-            s.live = 1;
-            s.pair = 0;
-            s.ntiles = min(r.nt - t, e - pos);
-            s.row0 = b;
-            s.kvh = g;
-            s.mA = s.mB = p.G;
-            s.partA = suffix_base + ((int)blockIdx.x + b * p.Hkv + g) * 2 * p.G;
-            s.partB = s.partA + p.G;
-            key0 = r.start * p.blk + t * TILE;
-            key_end = len;
-            trow = b;
-            mrows = p.G;
-            pg0 = t == 0 ? pgA : page_of(b, key0, len);
-            pg1 = t == 0 ? pgB : page_of(b, key0 + SUB, len);
-          }
+        // the first tile that begins at pos or behind it
+        const int item = local / ic, t = (local - item * ic + g.cost - 1) / g.cost;
+        pos = g.off + item * ic + t * g.cost;
+        if (t == g.nt || pos >= e) continue;
+        const int pair = item % g.npairs, i0 = pair * 2 * TILE;
+        const int left = g.nrows * p.G - i0;
+        s.live = 1;
+        s.pair = left > TILE;
+        s.ntiles = min(g.nt - t, (e - pos + g.cost - 1) / g.cost);
+        s.row0 = g.row0 + i0 / p.G;
+        s.kvh = item / g.npairs;
+        s.mA = min(left, TILE);
+        s.mB = s.pair ? min(left - TILE, TILE) : s.mA;
+        s.partA = g.base + ((int)blockIdx.x - g.cf + item) * g.rows;
+        s.partB = s.partA + (!s.pair && g.npairs == 1 ? s.mA : TILE);
+        s.check = 1;
+        key0 = t * TILE;
+        key_end = g.nb << shift;
+        trow = g.leader;
+        mrows = TILE;
+        pg = page_of(trow, key0, key_end);
+        pos += s.ntiles * g.cost;
+        break;
+      }
+      while (!s.live && pos < e) {
+        if (b < 0) {
+          b = max(at - p.n_groups, 0);
+          r = p.ws.row[b];
+          len = clamped(p.lengths[b]);
+          next_row();
+          pg_row = page_of(b, r.start << shift, len);
         }
-        s.base = slots / 2;
-        s.flip = nseg & 1;
-        s.qph = (qn[0] & 1) | (qn[1] & 1) << 1;
-        // the record, then the first tile, the queries, and the other tiles
-        const int sl = nseg % NSEG;
-        if (!mbar_wait(&ms->seg_empty[sl], ((uint32_t)(nseg / NSEG) & 1u) ^ 1u, abort_flag)) {
-          ok = false;
-          break;
+        int local = pos - me.prefix_cost - r.off;
+        if (local >= own_cost(r.nt) * p.Hkv) {
+          if (b + 1 >= p.B) {                    // cannot happen: a place has an item
+            pos = e;
+            break;
+          }
+          next_pages();
+          ++b;
+          r = nr;
+          len = clamped(nlen);
+          pg_row = npg_row;
+          npg = false;
+          next_row();
+          continue;
         }
+        const int ic = own_cost(r.nt), g = local / ic, base = pos - local + g * ic;
+        local -= g * ic;
+        // the first tile that begins at pos or behind it, and the first behind the share
+        const int t = local == 0 ? 0 : max((local - kSegCost + kOwnCost - 1) / kOwnCost, 1);
+        const int te = min(max((e - base - kSegCost + kOwnCost - 1) / kOwnCost, 1), r.nt);
+        pos = base + (t >= r.nt ? ic : own_begin(t));
+        if (t >= r.nt || pos >= e) continue;
+        s.live = 1;
+        s.pair = 0;
+        s.ntiles = te - t;
+        s.row0 = b;
+        s.kvh = g;
+        s.mA = s.mB = p.G;
+        s.partA = suffix_base + ((int)blockIdx.x + b * p.Hkv + g) * 2 * p.G;
+        s.partB = s.partA + p.G;
+        key0 = (r.start << shift) + t * TILE;
+        key_end = len;
+        trow = b;
+        mrows = p.G;
+        pg = t == 0 ? pg_row : page_of(b, key0, len);
+        pos = base + (te == r.nt ? ic : own_begin(te));
+      }
+      s.base = slots / 2;
+      // Tile T of single segments is stream T & 1's, so that a stream's next tile is never
+      // more than two on: its K is then loaded into a slot that an earlier tile frees.
+      s.flip = s.base & 1;
+      s.qslot = nseg & 1;
+      s.qn[0] = qn[0];
+      s.qn[1] = qn[1];
+      // the record, then the first key tile, the queries, and the other tiles
+      const int sl = nseg % NSEG;
+      if (!wwait(&ms->seg_empty[sl], ((uint32_t)(nseg / NSEG) & 1u) ^ 1u)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
         ms->seg[sl] = s;
         mbar_arrive(&ms->seg_full[sl]);
-        if (!s.live) break;
-        for (int t = 0; t < s.ntiles && ok; ++t) {
-          const int k0 = key0 + t * TILE;
-          const int pg[2] = {pg0, pg1};
-          if (t + 1 < s.ntiles) {
-            pg0 = page_of(trow, k0 + TILE, key_end);
-            pg1 = page_of(trow, k0 + TILE + SUB, key_end);
+      }
+      __syncwarp();
+      if (!s.live) break;
+      int npages = -2;                           // the lane's page of the next 16 tiles
+      const int u = lane & 1, hb = (lane >> 1) * 64;   // the lane's box: key half, dims
+      for (int t = 0; t < s.ntiles && ok; ++t) {
+        const int k0 = key0 + t * TILE, i = t & 15;
+        if (i == 0) {
+          if (t > 0) pg = npages;
+          npages = page_of(trow, k0 + 16 * TILE, key_end);
+        }
+        const int pg0 = __shfl_sync(0xffffffffu, pg, 2 * i);
+        const int pg1 = __shfl_sync(0xffffffffu, pg, 2 * i + 1);
+        int nv0 = max(min(key_end - k0, SUB), 0), nv1 = max(min(key_end - k0 - SUB, SUB), 0);
+        if ((nv0 > 0 && (unsigned)pg0 >= (unsigned)p.n_pages) ||
+            (nv1 > 0 && (unsigned)pg1 >= (unsigned)p.n_pages)) {
+          if (lane == 0) set_status(p.status, ETA_DEVSTAT_BAD_BLOCK);
+          if ((unsigned)pg0 >= (unsigned)p.n_pages) nv0 = 0;
+          if ((unsigned)pg1 >= (unsigned)p.n_pages) nv1 = 0;
+        }
+        const uint32_t bytes = (uint32_t)(((nv0 > 0) + (nv1 > 0)) * C::NH * (HALF / 2));
+        const bool mine = lane < 2 * C::NH && (u ? nv1 : nv0) > 0;
+        const int key = k0 + u * SUB;
+        const int y = (((u ? pg1 : pg0) * p.Hkv + s.kvh) << shift) + (key & (p.blk - 1));
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {            // K, then V
+          const int st = slots % C::NSLOT;
+          if (!wwait(&ms->kv_empty[st], ((uint32_t)(slots / C::NSLOT) & 1u) ^ 1u)) {
+            ok = false;
+            break;
           }
-          int nv[2] = {max(min(key_end - k0, SUB), 0), max(min(key_end - k0 - SUB, SUB), 0)};
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-            if (nv[u] > 0 && (pg[u] < 0 || pg[u] >= p.n_pages)) {
-              set_status(p.status, ETA_DEVSTAT_BAD_BLOCK);
-              nv[u] = 0;
-            }
-          const uint32_t bytes = (uint32_t)(((nv[0] > 0) + (nv[1] > 0)) * C::NH * (HALF / 2));
-#pragma unroll
-          for (int v = 0; v < 2 && ok; ++v) {    // K, then V
-            const int st = slots % C::NSLOT;
-            if (!mbar_wait(&ms->kv_empty[st], ((uint32_t)(slots / C::NSLOT) & 1u) ^ 1u,
-                           abort_flag)) {
-              ok = false;
-              break;
-            }
-            if (v) ms->nv[st] = make_int2(nv[0], nv[1]);
+          if (lane == 0) {
+            if (v) ms->nv[st] = make_int2(nv0, nv1);
             mbar_arrive_expect_tx(&ms->kv_full[st], bytes);
-            unsigned char* to = smem + C::OFF_KV + st * C::SLOT;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              if (nv[u] == 0) continue;
-              const int y = (pg[u] * p.Hkv + s.kvh) * p.blk + (k0 + u * SUB) % p.blk;
-#pragma unroll
-              for (int h = 0; h < C::NH; ++h)
-                tma_load_2d(to + h * HALF + u * (HALF / 2), v ? &tmV : &tmK, h * 64, y,
-                            &ms->kv_full[st]);
-            }
-            ++slots;
-            if (t == 0 && v == 0) {
-              // query slots: a pair fills both, a single segment the one of its number
-              for (int x = 0; x < 2 && ok; ++x) {
-                if (!s.pair && x != s.flip) continue;
-                if (!mbar_wait(&ms->q_empty[x], ((uint32_t)qn[x] & 1u) ^ 1u, abort_flag)) {
-                  ok = false;
-                  break;
-                }
+            __threadfence_block();
+            *(volatile int*)&ms->issued = slots + 1;
+          }
+          __syncwarp();
+          unsigned char* to = smem + C::OFF_KV + st * C::SLOT + (lane >> 1) * HALF + u * (HALF / 2);
+          if (mine) {
+            if (v) tma_load_2d(to, &tmV, hb, y, &ms->kv_full[st]);
+            else tma_load_2d(to, &tmK, hb, y, &ms->kv_full[st]);
+          }
+          ++slots;
+          if (t == 0 && v == 0) {
+            // query slots: a pair fills both, a single segment the one of its number
+            for (int x = 0; x < 2; ++x) {
+              if (!s.pair && x != s.qslot) continue;
+              if (!wwait(&ms->q_empty[x], ((uint32_t)qn[x] & 1u) ^ 1u)) {
+                ok = false;
+                break;
+              }
+              if (lane == 0) {
                 mbar_arrive_expect_tx(&ms->q_full[x], (uint32_t)(mrows * 128 * C::NH));
-                ++qn[x];
-                const int row = s.row0 + (s.pair && x ? TILE / p.G : 0);
-#pragma unroll
-                for (int h = 0; h < C::NH; ++h)
-                  tma_load_3d(smem + C::OFF_Q + x * C::SLOT + h * HALF, s.check ? &tmQ : &tmQ1,
-                              h * 64, s.kvh * p.G, row, &ms->q_full[x]);
+                __threadfence_block();
+                *(volatile int*)&ms->q_issued[x] = qn[x] + 1;
+              }
+              __syncwarp();
+              ++qn[x];
+              const int row = s.row0 + (s.pair && x ? TILE / p.G : 0);
+              if (lane < C::NH) {
+                unsigned char* q = smem + C::OFF_Q + x * C::SLOT + lane * HALF;
+                if (s.check) tma_load_3d(q, &tmQ, lane * 64, s.kvh * p.G, row, &ms->q_full[x]);
+                else tma_load_3d(q, &tmQ1, lane * 64, s.kvh * p.G, row, &ms->q_full[x]);
               }
             }
+            if (!ok) break;
           }
         }
-        pos += s.ntiles;
-        ++nseg;
-        if (b >= 0 && !npg && b + 1 < p.B) {     // the next row's record is here by now
-          npgA = page_of(b + 1, nr.start * p.blk, clamped(nlen));
-          npgB = page_of(b + 1, nr.start * p.blk + SUB, clamped(nlen));
-          npg = true;
-        }
       }
-      if (!ok) {
-        // wait (bounded) for every copy this thread issued before the CTA exits
-        set_status(p.status, ETA_DEVSTAT_TIMEOUT);
-        *abort_flag = 1;
-        for (int k = max(0, slots - C::NSLOT); k < slots; ++k)
-          mbar_wait(&ms->kv_full[k % C::NSLOT], (uint32_t)(k / C::NSLOT) & 1u, nullptr);
-        for (int x = 0; x < 2; ++x)
-          if (qn[x] > 0) mbar_wait(&ms->q_full[x], (uint32_t)(qn[x] - 1) & 1u, nullptr);
-      }
+      ++nseg;
+      if (b >= 0) next_pages();                  // the next row's record is here by now
     }
-  } else if (warp == 9) {
-    // ------------------------------------------------------------------ MMA issuer
-    // Event driven: each stream steps through its segments by itself, Q K^T once its S
-    // columns (P of the job before) are free, P V once the softmax has written P; one
-    // stream's wait never holds up the other.
+    if (!ok) {
+      // wait (bounded) for every copy this warp issued before the CTA exits
+      if (lane == 0) set_status(p.status, ETA_DEVSTAT_TIMEOUT);
+      *abort_flag = 1;
+      for (int k = max(0, slots - C::NSLOT); k < slots; ++k)
+        mbar_wait(&ms->kv_full[k % C::NSLOT], (uint32_t)(k / C::NSLOT) & 1u, nullptr);
+      for (int x = 0; x < 2; ++x)
+        if (qn[x] > 0) mbar_wait(&ms->q_full[x], (uint32_t)(qn[x] - 1) & 1u, nullptr);
+    }
+    __syncwarp();
+  } else if (warp > 8) {
+    // ------------------------------------------------------------------ MMA issuers
+    // One warp for each stream, so that one stream's waits never hold up the other: Q K^T
+    // once the stream's S columns (P of the job before) are free, P V once P is written.
+    const int x = warp - 9;
     if (lane == 0) {
-      Seg s[2];
-      int nseg[2] = {0, 0}, jobs[2] = {0, 0};    // the stream's segment, and its jobs there
-      int qk[2] = {0, 0}, pv[2] = {0, 0};        // of which issued
-      int cnt[2] = {0, 0}, used[2] = {0, 0};     // jobs, and segments with jobs, before it
-      bool open[2] = {false, false}, over[2] = {false, false};
-      const uint32_t q0 = smem_u32(smem + C::OFF_Q), kv0 = smem_u32(smem + C::OFF_KV);
       bool ok = true;
-      uint32_t idle = 0;
-      while (ok && !(over[0] && over[1])) {
-        bool did = false;
+      const uint64_t dq = smem_desc(smem_u32(smem + C::OFF_Q), 16, 1024, tc::kSwizzle128);
+      const uint64_t dk = smem_desc(smem_u32(smem + C::OFF_KV), 16, 1024, tc::kSwizzle128);
+      const uint64_t dv = smem_desc(smem_u32(smem + C::OFF_KV), HALF, 1024, tc::kSwizzle128);
+      const uint32_t tSx = tS[0] + x * 128, tOx = tO[0] + x * 128;
+      constexpr uint32_t id = idesc<D>() | (1u << 16);           // V is MN-major
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return mbar_wait(bar, parity, abort_flag);
+      };
+      auto load_in = [&](uint64_t* bar, int n, volatile int* issued, int item) -> bool {
+        return wait_load(bar, n, issued, item, abort_flag);
+      };
+      // Two cursors over the stream's half tiles: Q K^T runs two ahead of P V, into the next
+      // segment where one ends.  n: jobs so far.
+      struct Cursor {
+        Seg s;
+        int nseg, jobs, j, h, n;
+        bool over;
+      };
+      Cursor q = {}, v = {};
+      int used = 0;                              // segments with jobs before v's
+      // The segment of the cursor's next half tile; `enter` is called for every segment.
+      auto settle = [&](Cursor& c, auto enter, auto leave) -> bool {
+        while (!c.over && c.j >= c.jobs) {
+          if (c.nseg > 0) leave();
+          const int sl = c.nseg % NSEG;
+          if (!wait(&ms->seg_full[sl], (uint32_t)(c.nseg / NSEG) & 1u)) return false;
+          c.s = ms->seg[sl];
+          c.over = !c.s.live;
+          if (c.over) break;
+          ++c.nseg;
+          c.jobs = jobs_of(c.s, x);
+          c.j = c.h = 0;
+          if (!enter()) return false;
+        }
+        return true;
+      };
+      auto step = [](Cursor& c) {
+        if ((c.h ^= 1) == 0) {
+          ++c.j;
+          ++c.n;
+        }
+      };
+      auto issue_qk = [&]() -> bool {            // S_h = Q K_h^T of q's half tile
+        if (!settle(
+                q,
+                [&]() -> bool {
+                  const int qs = q.s.pair ? x : q.s.qslot;
+                  if (q.jobs > 0)
+                    return load_in(&ms->q_full[qs], q.s.qn[qs], &ms->q_issued[qs], q.s.qn[qs]);
+                  // A single segment of one tile, nothing for this stream to take: its
+                  // arrival must not count for the slot's queries before these.
+                  if (!wait_issued(&ms->q_issued[qs], q.s.qn[qs], abort_flag)) return false;
+                  mbar_arrive(&ms->q_empty[qs]);
+                  return true;
+                },
+                [] {}))
+          return false;
+        if (q.over) return true;
+        const int T = q.s.base + tile_of(q.s, x, q.j), ks = C::kslot(T);
+        const int qs = q.s.pair ? x : q.s.qslot;
+        if (q.h == 0 && !load_in(&ms->kv_full[ks], C::kload(T), &ms->issued, 2 * T)) return false;
+        // S_h's columns hold P of the job before until P V has read it
+        if (q.n > 0 && !wait(&ms->pv_done[x][q.h], (uint32_t)(q.n - 1) & 1u)) return false;
+        tc_fence_after();
+        const uint64_t dqs = dq + (uint64_t)(qs * C::SLOT >> 4);
+        const uint64_t dks = dk + (uint64_t)((ks * C::SLOT + q.h * (HALF / 2)) >> 4);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (over[x]) continue;
-          if (!open[x]) {                        // the stream's next segment
-            const int sl = nseg[x] % NSEG;
-            if (!mbar_test(&ms->seg_full[sl], (uint32_t)(nseg[x] / NSEG) & 1u)) continue;
-            s[x] = ms->seg[sl];
-            did = true;
-            if (!s[x].live) {
-              over[x] = true;
-              continue;
-            }
-            jobs[x] = jobs_of(s[x], x);
-            qk[x] = pv[x] = 0;
-            open[x] = true;
-            if (nseg[x ^ 1] <= nseg[x] && !(open[x ^ 1] && nseg[x ^ 1] == nseg[x])) {
-              // the first of the two streams to get here
-              ms->left[sl][0] = ms->left[sl][1] = s[x].ntiles;
-              ms->both[sl] = 0;
-            }
-          }
-          const int sl = nseg[x] % NSEG;
-          // P V of the oldest job whose S is out
-          if (pv[x] < qk[x] && mbar_test(&ms->p_full[x], (uint32_t)(cnt[x] + pv[x]) & 1u) &&
-              (pv[x] > 0 || used[x] == 0 ||
-               mbar_test(&ms->o_free[x], (uint32_t)(used[x] - 1) & 1u))) {
-            const int tile = tile_of(s[x], x, pv[x]), T = s[x].base + tile;
-            // long over, the softmax waited for it: makes V visible to this thread
-            if (!mbar_test(&ms->kv_full[C::vslot(T)], C::vphase(T))) continue;
-            tc_fence_after();
-            const uint32_t va = kv0 + C::vslot(T) * C::SLOT;
-            constexpr uint32_t id = idesc<D>() | (1u << 16);           // V is MN-major
-#pragma unroll
-            for (int term = 0; term < NS; ++term)
-#pragma unroll
-              for (int kk = 0; kk < TILE / 16; ++kk)
-                mma_f16_ts(tO[x],
-                           tS[x] + (NS == 1 ? kk * 8 : (kk >> 1) * 32 + term * 16 + (kk & 1) * 8),
-                           smem_desc(va + kk * 2048, HALF, 1024, tc::kSwizzle128), id,
-                           (pv[x] > 0 || term > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(&ms->pv_done[x]);
-            ++pv[x];
-            // a pair's tile is done with when both streams have taken it
-            if (!s[x].pair || nseg[x ^ 1] > nseg[x] ||
-                (open[x ^ 1] && nseg[x ^ 1] == nseg[x] && pv[x ^ 1] > tile))
-              mma_commit(&ms->kv_empty[C::vslot(T)]);
-            did = true;
-          }
-          // Q K^T of the next job
-          if (qk[x] < jobs[x] && qk[x] == pv[x] &&
-              (cnt[x] + qk[x] == 0 ||
-               mbar_test(&ms->pv_done[x], (uint32_t)(cnt[x] + qk[x] - 1) & 1u))) {
-            const int tile = tile_of(s[x], x, qk[x]), T = s[x].base + tile;
-            const int qs = s[x].pair ? x : s[x].flip;
-            if (mbar_test(&ms->kv_full[C::kslot(T)], C::kphase(T)) &&
-                mbar_test(&ms->q_full[qs], (uint32_t)(s[x].qph >> qs) & 1u)) {
-              tc_fence_after();
-              const uint32_t ka = kv0 + C::kslot(T) * C::SLOT, qa = q0 + qs * C::SLOT;
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (uint32_t)(kk >> 2) * HALF + (uint32_t)(kk & 3) * 32;
-                mma_f16(tS[x], smem_desc(qa + off, 16, 1024, tc::kSwizzle128),
-                        smem_desc(ka + off, 16, 1024, tc::kSwizzle128), idesc<TILE>(), kk > 0);
-              }
-              mma_commit(&ms->s_full[x]);
-              ++qk[x];
-              if (!s[x].pair || nseg[x ^ 1] > nseg[x] ||
-                  (open[x ^ 1] && nseg[x ^ 1] == nseg[x] && qk[x ^ 1] > tile))
-                mma_commit(&ms->kv_empty[C::kslot(T)]);
-              if (--ms->left[sl][qs] == 0) mma_commit(&ms->q_empty[qs]);
-              did = true;
-            }
-          }
-          if (pv[x] == jobs[x]) {                // on to the next segment
-            cnt[x] += jobs[x];
-            used[x] += jobs[x] > 0;
-            ++nseg[x];
-            open[x] = false;
-            if (++ms->both[sl] == 2) mbar_arrive(&ms->seg_empty[sl]);
-            did = true;
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t off = (uint64_t)(((kk >> 2) * HALF + (kk & 3) * 32) >> 4);
+          mma_f16(tSx + q.h * SUB, dqs + off, dks + off, idesc<SUB>(), kk > 0);
+        }
+        mma_commit(&ms->s_full[x][q.h]);
+        if (q.h) {
+          // a tile's slot is free after two arrivals: a pair's streams each give one
+          mma_commit(&ms->kv_empty[ks]);
+          if (!q.s.pair) mma_commit(&ms->kv_empty[ks]);
+          if (q.j == q.jobs - 1) {
+            mma_commit(&ms->q_empty[qs]);
+            if (q.s.pair) mma_commit(&ms->q_empty[qs]);
           }
         }
-        if (did) {
-          idle = 0;
-        } else if (++idle > kIdleLimit || *abort_flag) {
-          ok = false;
+        step(q);
+        return true;
+      };
+      auto issue_pv = [&]() -> bool {            // O += P_h V_h of v's half tile
+        const int T = v.s.base + tile_of(v.s, x, v.j), vs = C::vslot(T);
+        // the stream's last segment has to be read out of O before O begins anew
+        if (v.j == 0 && v.h == 0 && used > 0 &&
+            !wait(&ms->o_free[x], (uint32_t)(used - 1) & 1u))
+          return false;
+        if (!wait(&ms->p_full[x][v.h], (uint32_t)v.n & 1u) ||
+            !wait(&ms->kv_full[vs], (uint32_t)C::vload(T) & 1u))
+          return false;
+        tc_fence_after();
+        const uint64_t dvs = dv + (uint64_t)((vs * C::SLOT + v.h * (HALF / 2)) >> 4);
+#pragma unroll
+        for (int term = 0; term < NS; ++term)
+#pragma unroll
+          for (int kk = 0; kk < SUB / 16; ++kk)
+            mma_f16_ts(tOx, tSx + v.h * SUB + term * 32 + kk * 8, dvs + (uint64_t)(kk * 2048 >> 4),
+                       id, (term > 0 || kk > 0) ? 1u : (uint32_t)(v.j + v.h > 0));
+        mma_commit(&ms->pv_done[x][v.h]);
+        if (v.h) {
+          mma_commit(&ms->kv_empty[vs]);
+          if (!v.s.pair) mma_commit(&ms->kv_empty[vs]);
         }
+        step(v);
+        return true;
+      };
+      ok = issue_qk() && issue_qk();
+      while (ok) {
+        ok = settle(v, [] { return true; },
+                    [&] {
+                      used += v.jobs > 0;
+                      mbar_arrive(&ms->seg_empty[(v.nseg - 1) % NSEG]);
+                    });
+        if (!ok || v.over) break;
+        ok = issue_pv() && issue_qk();
       }
       if (!ok) {
         set_status(p.status, ETA_DEVSTAT_TIMEOUT);
         *abort_flag = 1;
       }
-      mma_commit(&ms->fin);
-      mbar_wait(&ms->fin, 0, nullptr);
+      // every MMA issued so far has completed before TMEM is released
+      mma_commit(&ms->fin[x]);
+      mbar_wait(&ms->fin[x], 0, nullptr);
     }
   } else {
     // ------------------------------------------------------------------ softmax
@@ -834,7 +905,8 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
       const int mine = x == 0 ? s.mA : s.mB;
       const bool active = (warp & 3) * 32 < mine;      // the warp has a valid row
       const int b = s.row0 + (i + (s.pair && x ? TILE : 0)) / p.G, h = s.kvh * p.G + i % p.G;
-      const bool valid = i < mine;
+      const bool valid = i < mine && ETA_IN_BOUNDS(b, p.B, p.status) &&
+                         ETA_IN_BOUNDS(h, p.Hq, p.status);
       // Gated logits in raw units u (the gated logit is scale * u), so that the scale
       // folds into the constants: the hard gate keeps s iff s >= tau / scale; the soft
       // gate is hs + hs * tanh(s * ta - tb), hs = s / 2, for a bf16 output (one
@@ -854,16 +926,15 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
       const int jobs = jobs_of(s, x);
       for (int j = 0; j < jobs; ++j, ++cnt) {
         const int T = s.base + tile_of(s, x, j);
-        // V's slot is not loaded again before this tile's P V: its phase is this tile's
-        if (!wwait(&ms->s_full[x], (uint32_t)cnt & 1u) ||
-            !wwait(&ms->kv_full[C::vslot(T)], C::vphase(T))) {
+        // V's slot is not loaded again before this tile's P V
+        if (!wwait(&ms->s_full[x][0], (uint32_t)cnt & 1u) ||
+            !__all_sync(0xffffffffu, wait_load(&ms->kv_full[C::vslot(T)], C::vload(T),
+                                               &ms->issued, 2 * T + 1, abort_flag))) {
           ok = false;
           break;
         }
-        tc_fence_after();
         const int2 nv = ms->nv[C::vslot(T)];
-        const bool partial = nv.x < SUB || nv.y < SUB;
-        if (partial) {                           // V rows past the end must be finite
+        if (nv.x < SUB || nv.y < SUB) {          // V rows past the end must be finite
           if ((i & (SUB - 1)) >= (i < SUB ? nv.x : nv.y)) {
             unsigned char* vt = smem + C::OFF_KV + C::vslot(T) * C::SLOT + i * 128;
 #pragma unroll
@@ -874,56 +945,33 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
           }
           fence_async_smem();
         }
-        if (active) {
-          uint32_t P[NS == 1 ? 64 : 1];
-          bool again = NS == 2 || j == 0 || partial;
-          if constexpr (NS == 1) {
-            // One pass with the maximum of the tiles before: a weight may exceed 1, by
-            // e^kRescale at most; if any does by more the tile is done again below (S is
-            // still there: P waits in registers).
-            if (!again) {
-              float va[32], vb[32], pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-              float2 ln = l2;
-              const float nm = m == -INFINITY ? 0.f : -m * c1;
-              tmem_ld32(tSx, va);
-              tmem_wait_ld32(va);
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                float* v = c & 1 ? vb : va;
-                float* w = c & 1 ? va : vb;
-                if (c < 3) tmem_ld32(tSx + (c + 1) * 32, w);
-                gate32<GATE, NS>(v, ga);
-                max32(v, pm);
-                exp32<1>(v, c1, nm, ln, P + 16 * c, nullptr);
-                if (c < 3) tmem_wait_ld32(w);
-              }
-              const float mx = fmaxf(fmax3(pm[0], pm[1], pm[2]), pm[3]);
-              again = __any_sync(0xffffffffu, valid && mx > m + resc_raw);
-              if (!again) l2 = ln;
-            }
+#pragma unroll 1
+        for (int hf = 0; hf < 2; ++hf) {
+          if (hf && !wwait(&ms->s_full[x][1], (uint32_t)cnt & 1u)) {
+            ok = false;
+            break;
           }
-          if (again) {
-            // the tile's maximum first; gated and masked scores go back into S
-            float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          tc_fence_after();
+          if (active) {
+            const uint32_t tSh = tSx + hf * SUB;
+            const int lim = hf ? nv.y : nv.x;
+            float sv[SUB];
+            tmem_ld32(tSh, sv);
+            tmem_ld32(tSh + 32, sv + 32);
+            tmem_wait_ld32(sv);
+            tmem_wait_ld32(sv + 32);
+            gate32<GATE, NS>(sv, ga);
+            gate32<GATE, NS>(sv + 32, ga);
+            if (lim < SUB) {                     // keys past the end
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float v[32];
-              tmem_ld32(tSx + c * 32, v);
-              tmem_wait_ld32(v);
-              gate32<GATE, NS>(v, ga);
-              if (partial) {
-                const int lim = (c < 2 ? nv.x : nv.y) - (c & 1) * 32;
-#pragma unroll
-                for (int u = 0; u < 32; ++u)
-                  if (u >= lim) v[u] = -INFINITY;
-              }
-              max32(v, pm);
-              if (GATE != NONE || partial)
-                tmem_st32(tSx + c * 32, reinterpret_cast<const uint32_t*>(v));
+              for (int c = 0; c < SUB; ++c)
+                if (c >= lim) sv[c] = -INFINITY;
             }
+            float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            max32(sv, pm);
+            max32(sv + 32, pm);
             const float mx = fmaxf(fmax3(pm[0], pm[1], pm[2]), pm[3]);
-            if (GATE != NONE || partial) tmem_wait_st();
-            // the first tile sets the maximum; later ones rescale O (in TMEM) only when it
+            // the first keys set the maximum; later ones rescale O (in TMEM) only when it
             // grew by more than kRescale
             float alpha = 1.f;
             bool resc = false;
@@ -934,8 +982,13 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
               m = mx;
               resc = true;
             }
-            if (__any_sync(0xffffffffu, resc)) {
-              // P V of the stream's previous job is complete: this Q K^T waited for it
+            if (__any_sync(0xffffffffu, resc && valid)) {
+              // P V of the half tile before has to be complete
+              if (!wwait(&ms->pv_done[x][hf ^ 1], (uint32_t)(hf ? cnt : cnt - 1) & 1u)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
 #pragma unroll
               for (int c = 0; c < D / 32; ++c) {
                 float ov[32];
@@ -949,35 +1002,23 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
               l2.y *= alpha;
             }
             const float nm = m == -INFINITY ? 0.f : -m * c1;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float v[32];
-              tmem_ld32(tSx + c * 32, v);
-              tmem_wait_ld32(v);
-              if constexpr (NS == 1) {
-                exp32<1>(v, c1, nm, l2, P + 16 * c, nullptr);
-              } else {                           // both terms into the chunk's own columns
-                uint32_t hi[16], lo[16];
-                exp32<2>(v, c1, nm, l2, hi, lo);
-                tmem_st16(tSx + c * 32, hi);
-                tmem_st16(tSx + c * 32 + 16, lo);
-              }
-            }
+            uint32_t hi[32], lo[NS == 2 ? 32 : 1];
+            exp32<NS>(sv, c1, nm, l2, hi, lo);
+            exp32<NS>(sv + 32, c1, nm, l2, hi + 16, NS == 2 ? lo + 16 : lo);
+            tmem_st32(tSh, hi);
+            if constexpr (NS == 2) tmem_st32(tSh + 32, lo);
+            tmem_wait_st();
           }
-          if constexpr (NS == 1) {
-            tmem_st32(tSx, P);
-            tmem_st32(tSx + 32, P + 32);
-          }
-          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms->p_full[x][hf]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ms->p_full[x]);
+        if (!ok) break;
       }
       if (!ok) break;
       // the segment's partial result of this stream
       if (jobs > 0) {
-        if (!wwait(&ms->pv_done[x], (uint32_t)(cnt - 1) & 1u)) { ok = false; break; }
+        if (!wwait(&ms->pv_done[x][1], (uint32_t)(cnt - 1) & 1u)) { ok = false; break; }
         tc_fence_after();
       }
       if (active) {
@@ -1053,8 +1094,8 @@ shared_combine_kernel(const AttendParams p, OutT* __restrict__ o, float* __restr
     const GroupRec g = p.ws.grp[r.group];
     const int i = (b - g.row0) * G, pair = i / (2 * TILE), ii = i % (2 * TILE);
     const int item = kvh * g.npairs + pair, left = g.nrows * G - pair * 2 * TILE;
-    const int a = g.off + item * g.nt, c0 = a / hd.share;
-    n1 = (a + g.nt - 1) / hd.share - c0 + 1;
+    const int a = g.off + item * g.nt * g.cost, c0 = a / hd.share;
+    n1 = (a + (g.nt - 1) * g.cost) / hd.share - c0 + 1;
     first1 = g.base + (c0 - g.cf + item) * g.rows + ii;
     step1 = g.rows;
     two1 = left <= TILE;
@@ -1062,8 +1103,8 @@ shared_combine_kernel(const AttendParams p, OutT* __restrict__ o, float* __restr
   }
   int n2 = 0, first2 = 0;                                   // the row's own slots
   if (r.nt > 0) {
-    const int a = p.ws.cta[0].prefix_units + r.off + kvh * r.nt, c0 = a / hd.share;
-    n2 = (a + r.nt - 1) / hd.share - c0 + 1;
+    const int a = p.ws.cta[0].prefix_cost + r.off + kvh * own_cost(r.nt), c0 = a / hd.share;
+    n2 = (a + own_begin(r.nt - 1)) / hd.share - c0 + 1;
     first2 = hd.suffix_base + (c0 + b * p.Hkv + kvh) * 2 * G;
   }
   const int m1 = n1 * (1 + two1), n = min(m1 + 2 * n2, kMaxSlots);
@@ -1179,11 +1220,11 @@ inline WsOff ws_off(const eta_dims_t* d, int n_groups, int P) {
 
 inline int grid_size() { return std::max(sm_count(), 1); }
 
-// Sizes whose unit counts fit 32-bit sums, and whose parts fit the combine's list.
+// Sizes whose costs fit 32-bit sums, and whose parts fit the combine's list.
 inline eta_status_t check_sizes(const eta_dims_t* d, int32_t n_groups, int P) {
   if (n_groups < 1 || n_groups > d->B) return ETA_ERR_INVALID_ARG;
   const uint64_t tiles = ((uint64_t)d->T_max + TILE - 1) / TILE;
-  if (2 * tiles * d->B * d->Hkv >= (1ull << 31)) return ETA_ERR_UNSUPPORTED;
+  if (16 * tiles * d->B * d->Hkv >= (1ull << 31)) return ETA_ERR_UNSUPPORTED;
   if ((uint64_t)P * 528 + 4ull * d->B * d->Hq >= (1ull << 31)) return ETA_ERR_UNSUPPORTED;
   if (4 * P > kMaxSlots) return ETA_ERR_UNSUPPORTED;
   return ETA_OK;
