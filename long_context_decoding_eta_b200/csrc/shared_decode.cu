@@ -276,9 +276,19 @@ struct Seg {
   int partA, partB;     // first partial row of each stream
   int check;            // prefix: rows that do not share it are left out
   int flip;             // single: the stream of the first key tile
-  int qslot;            // single: the query slot
-  int qn[2];            // loads of each query slot before the segment's
 };
+
+// What the MMA warps need of a key tile, a word per tile in a ring: written before the
+// tile's K is counted in `issued`.
+enum TileFlags {
+  kPairTile = 1,        // both streams take it; else stream T & 1
+  kFirst = 2,           // the first of its segment for every stream that takes it
+  kQSlot = 4,           // single: the query slot is 1
+  kQRel1 = 8,           // arrivals at the query slot's `empty` behind this tile's Q K^T: one,
+  kQRel2 = 16,          // or two
+  kQPhase0 = 32, kQPhase1 = 64,   // the phase of each query slot's load
+};
+constexpr int NTILE = 16;                       // tile words in flight (at most 7 are)
 
 // Jobs (key tiles) of stream x in a segment, and the tile of job j.
 ETA_DEV int jobs_of(const Seg& s, int x) {
@@ -294,7 +304,9 @@ struct Misc {
   uint64_t seg_full[NSEG], seg_empty[NSEG], fin[2];
   Seg seg[NSEG];
   int2 nv[NSLOT];       // of a V slot: valid keys of the tile's two 64-key halves
-  int issued, q_issued[2];   // K and V tiles, and queries of each slot, under way so far
+  int tile[NTILE];      // TileFlags
+  int issued;           // loads of K and V tiles under way so far
+  int end;              // key tiles of the CTA, once known
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -409,20 +421,15 @@ ETA_DEV void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
       : "memory");
 }
 
-// Waits for load number n (from 0) of a slot, which is number `item` of those that the
-// producer counts in *issued.  A wait for a phase's parity also ends while the phase before
-// it is open, and a stream does not follow the loads of the other's tiles: so first that
-// the load has been issued (the slot's loads before it are then over), then that it is in.
-ETA_DEV bool wait_issued(volatile int* issued, int item, volatile int* abort) {
+// Waits until load `item` (tile T's K is 2 T, its V 2 T + 1) has been issued; false too
+// when the CTA has no such tile.
+ETA_DEV bool wait_issued(volatile int* issued, volatile int* end, int item,
+                         volatile int* abort) {
   uint32_t polls = 0;
   while (*issued <= item)
-    if (++polls > kIssueLimit || *abort) return false;
+    if (*end <= item / 2 || ++polls > kIssueLimit || *abort) return false;
   __threadfence_block();
   return true;
-}
-ETA_DEV bool wait_load(uint64_t* bar, int n, volatile int* issued, int item,
-                       volatile int* abort) {
-  return wait_issued(issued, item, abort) && mbar_wait(bar, (uint32_t)n & 1u, abort);
 }
 
 // The gate on 32 scores of a query row, in raw units (see the softmax).
@@ -514,9 +521,10 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
     }
     for (int s = 0; s < NSEG; ++s) {
       mbar_init(&ms->seg_full[s], 1);
-      mbar_init(&ms->seg_empty[s], 10);         // 8 softmax warps and the MMA warps
+      mbar_init(&ms->seg_empty[s], 8);          // the softmax warps
     }
-    ms->issued = ms->q_issued[0] = ms->q_issued[1] = 0;
+    ms->issued = 0;
+    ms->end = 0x7fffffff;
     ms->abort_flag = 0;
     fence_mbar_init();
   }
@@ -655,9 +663,9 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
       // Tile T of single segments is stream T & 1's, so that a stream's next tile is never
       // more than two on: its K is then loaded into a slot that an earlier tile frees.
       s.flip = s.base & 1;
-      s.qslot = nseg & 1;
-      s.qn[0] = qn[0];
-      s.qn[1] = qn[1];
+      const int qslot = nseg & 1;
+      const int qflags = (s.pair ? kPairTile : qslot * kQSlot) | (qn[0] & 1) * kQPhase0 |
+                         (qn[1] & 1) * kQPhase1;
       // the record, then the first key tile, the queries, and the other tiles
       const int sl = nseg % NSEG;
       if (!wwait(&ms->seg_empty[sl], ((uint32_t)(nseg / NSEG) & 1u) ^ 1u)) {
@@ -668,8 +676,11 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
         ms->seg[sl] = s;
         mbar_arrive(&ms->seg_full[sl]);
       }
+      if (!s.live) {
+        if (lane == 0) *(volatile int*)&ms->end = s.base;
+        break;
+      }
       __syncwarp();
-      if (!s.live) break;
       int npages = -2;                           // the lane's page of the next 16 tiles
       const int u = lane & 1, hb = (lane >> 1) * 64;   // the lane's box: key half, dims
       for (int t = 0; t < s.ntiles && ok; ++t) {
@@ -699,7 +710,16 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
             break;
           }
           if (lane == 0) {
-            if (v) ms->nv[st] = make_int2(nv0, nv1);
+            if (v) {
+              ms->nv[st] = make_int2(nv0, nv1);
+            } else {
+              // both arrivals at a query slot come from the one stream that uses it, or
+              // one from each, behind its last tile
+              const int last = s.ntiles - 1 - t;
+              ms->tile[(slots / 2) % NTILE] =
+                  qflags | (t < (s.pair ? 1 : 2) ? kFirst : 0) |
+                  (s.pair || s.ntiles == 1 ? (last == 0 ? kQRel2 : 0) : (last < 2 ? kQRel1 : 0));
+            }
             mbar_arrive_expect_tx(&ms->kv_full[st], bytes);
             __threadfence_block();
             *(volatile int*)&ms->issued = slots + 1;
@@ -714,16 +734,13 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
           if (t == 0 && v == 0) {
             // query slots: a pair fills both, a single segment the one of its number
             for (int x = 0; x < 2; ++x) {
-              if (!s.pair && x != s.qslot) continue;
+              if (!s.pair && x != qslot) continue;
               if (!wwait(&ms->q_empty[x], ((uint32_t)qn[x] & 1u) ^ 1u)) {
                 ok = false;
                 break;
               }
-              if (lane == 0) {
+              if (lane == 0)
                 mbar_arrive_expect_tx(&ms->q_full[x], (uint32_t)(mrows * 128 * C::NH));
-                __threadfence_block();
-                *(volatile int*)&ms->q_issued[x] = qn[x] + 1;
-              }
               __syncwarp();
               ++qn[x];
               const int row = s.row0 + (s.pair && x ? TILE / p.G : 0);
@@ -762,119 +779,92 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
       const uint64_t dv = smem_desc(smem_u32(smem + C::OFF_KV), HALF, 1024, tc::kSwizzle128);
       const uint32_t tSx = tS[0] + x * 128, tOx = tO[0] + x * 128;
       constexpr uint32_t id = idesc<D>() | (1u << 16);           // V is MN-major
+      volatile int* issued = &ms->issued;
+      volatile int* end = &ms->end;
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
         return mbar_wait(bar, parity, abort_flag);
       };
-      auto load_in = [&](uint64_t* bar, int n, volatile int* issued, int item) -> bool {
-        return wait_load(bar, n, issued, item, abort_flag);
-      };
-      // Two cursors over the stream's half tiles: Q K^T runs two ahead of P V, into the next
-      // segment where one ends.  n: jobs so far.
-      struct Cursor {
-        Seg s;
-        int nseg, jobs, j, h, n;
-        bool over;
-      };
-      Cursor q = {}, v = {};
-      int used = 0;                              // segments with jobs before v's
-      // The segment of the cursor's next half tile; `enter` is called for every segment.
-      auto settle = [&](Cursor& c, auto enter, auto leave) -> bool {
-        while (!c.over && c.j >= c.jobs) {
-          if (c.nseg > 0) leave();
-          const int sl = c.nseg % NSEG;
-          if (!wait(&ms->seg_full[sl], (uint32_t)(c.nseg / NSEG) & 1u)) return false;
-          c.s = ms->seg[sl];
-          c.over = !c.s.live;
-          if (c.over) break;
-          ++c.nseg;
-          c.jobs = jobs_of(c.s, x);
-          c.j = c.h = 0;
-          if (!enter()) return false;
+      // The stream's next tile, from T on, and its flags; T = -1: no more.  A barrier's
+      // parity also looks over while the phase before is open, and a stream does not follow
+      // the loads of the other's tiles: that a load has been issued says that those before
+      // it into the same slot are over.  The queries' load is issued between the first
+      // tile's K and V.
+      auto find = [&](int& T, int& f) -> bool {
+        for (;; ++T) {
+          if (!wait_issued(issued, end, 2 * T, abort_flag)) {
+            ok = *end <= T;
+            T = -1;
+            return ok;
+          }
+          f = *(volatile int*)&ms->tile[T % NTILE];
+          if ((f & kPairTile) || (T & 1) == x) break;
         }
-        return true;
-      };
-      auto step = [](Cursor& c) {
-        if ((c.h ^= 1) == 0) {
-          ++c.j;
-          ++c.n;
+        if (f & kFirst) {
+          const int qs = (f & kPairTile) ? x : (f & kQSlot) ? 1 : 0;
+          ok = wait_issued(issued, end, 2 * T + 1, abort_flag) &&
+               wait(&ms->q_full[qs], (f & (qs ? kQPhase1 : kQPhase0)) ? 1u : 0u);
         }
+        return ok = ok && wait(&ms->kv_full[C::kslot(T)], (uint32_t)C::kload(T) & 1u);
       };
-      auto issue_qk = [&]() -> bool {            // S_h = Q K_h^T of q's half tile
-        if (!settle(
-                q,
-                [&]() -> bool {
-                  const int qs = q.s.pair ? x : q.s.qslot;
-                  if (q.jobs > 0)
-                    return load_in(&ms->q_full[qs], q.s.qn[qs], &ms->q_issued[qs], q.s.qn[qs]);
-                  // A single segment of one tile, nothing for this stream to take: its
-                  // arrival must not count for the slot's queries before these.
-                  if (!wait_issued(&ms->q_issued[qs], q.s.qn[qs], abort_flag)) return false;
-                  mbar_arrive(&ms->q_empty[qs]);
-                  return true;
-                },
-                [] {}))
-          return false;
-        if (q.over) return true;
-        const int T = q.s.base + tile_of(q.s, x, q.j), ks = C::kslot(T);
-        const int qs = q.s.pair ? x : q.s.qslot;
-        if (q.h == 0 && !load_in(&ms->kv_full[ks], C::kload(T), &ms->issued, 2 * T)) return false;
-        // S_h's columns hold P of the job before until P V has read it
-        if (q.n > 0 && !wait(&ms->pv_done[x][q.h], (uint32_t)(q.n - 1) & 1u)) return false;
+      // S_h = Q K_h^T of tile T, the stream's n-th
+      auto issue_qk = [&](int T, int f, int n, int h) {
+        // S_h's columns hold P of the tile before until P V has read it
+        if (ok && n > 0) ok = wait(&ms->pv_done[x][h], (uint32_t)(n - 1) & 1u);
+        if (!ok) return;
         tc_fence_after();
-        const uint64_t dqs = dq + (uint64_t)(qs * C::SLOT >> 4);
-        const uint64_t dks = dk + (uint64_t)((ks * C::SLOT + q.h * (HALF / 2)) >> 4);
+        const int ks = C::kslot(T), qs = (f & kPairTile) ? x : (f & kQSlot) ? 1 : 0;
+        const uint64_t dqs = dq + (uint64_t)(qs * (C::SLOT >> 4));
+        const uint64_t dks = dk + (uint64_t)(ks * (C::SLOT >> 4) + h * (HALF / 2 >> 4));
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t off = (uint64_t)(((kk >> 2) * HALF + (kk & 3) * 32) >> 4);
-          mma_f16(tSx + q.h * SUB, dqs + off, dks + off, idesc<SUB>(), kk > 0);
+          mma_f16(tSx + h * SUB, dqs + off, dks + off, idesc<SUB>(), kk > 0);
         }
-        mma_commit(&ms->s_full[x][q.h]);
-        if (q.h) {
+        mma_commit(&ms->s_full[x][h]);
+        if (h) {
           // a tile's slot is free after two arrivals: a pair's streams each give one
           mma_commit(&ms->kv_empty[ks]);
-          if (!q.s.pair) mma_commit(&ms->kv_empty[ks]);
-          if (q.j == q.jobs - 1) {
-            mma_commit(&ms->q_empty[qs]);
-            if (q.s.pair) mma_commit(&ms->q_empty[qs]);
-          }
+          if (!(f & kPairTile)) mma_commit(&ms->kv_empty[ks]);
+          if (f & (kQRel1 | kQRel2)) mma_commit(&ms->q_empty[qs]);
+          if (f & kQRel2) mma_commit(&ms->q_empty[qs]);
         }
-        step(q);
-        return true;
       };
-      auto issue_pv = [&]() -> bool {            // O += P_h V_h of v's half tile
-        const int T = v.s.base + tile_of(v.s, x, v.j), vs = C::vslot(T);
+      int segs = 0;                              // segments begun
+      // O += P_h V_h of tile T, the stream's n-th (V is in: the softmax waited for it)
+      auto issue_pv = [&](int T, int f, int n, int h) {
+        const bool first = h == 0 && (f & kFirst);
         // the stream's last segment has to be read out of O before O begins anew
-        if (v.j == 0 && v.h == 0 && used > 0 &&
-            !wait(&ms->o_free[x], (uint32_t)(used - 1) & 1u))
-          return false;
-        if (!wait(&ms->p_full[x][v.h], (uint32_t)v.n & 1u) ||
-            !wait(&ms->kv_full[vs], (uint32_t)C::vload(T) & 1u))
-          return false;
+        if (ok && first && segs++ > 0) ok = wait(&ms->o_free[x], (uint32_t)segs & 1u);
+        if (ok) ok = wait(&ms->p_full[x][h], (uint32_t)n & 1u);
+        const int vs = C::vslot(T);
+        if (!ok || !(ok = wait(&ms->kv_full[vs], (uint32_t)C::vload(T) & 1u))) return;
         tc_fence_after();
-        const uint64_t dvs = dv + (uint64_t)((vs * C::SLOT + v.h * (HALF / 2)) >> 4);
+        const uint64_t dvs = dv + (uint64_t)(vs * (C::SLOT >> 4) + h * (HALF / 2 >> 4));
 #pragma unroll
         for (int term = 0; term < NS; ++term)
 #pragma unroll
           for (int kk = 0; kk < SUB / 16; ++kk)
-            mma_f16_ts(tOx, tSx + v.h * SUB + term * 32 + kk * 8, dvs + (uint64_t)(kk * 2048 >> 4),
-                       id, (term > 0 || kk > 0) ? 1u : (uint32_t)(v.j + v.h > 0));
-        mma_commit(&ms->pv_done[x][v.h]);
-        if (v.h) {
+            mma_f16_ts(tOx, tSx + h * SUB + term * 32 + kk * 8, dvs + (uint64_t)(kk * 2048 >> 4),
+                       id, (term > 0 || kk > 0) ? 1u : first ? 0u : 1u);
+        mma_commit(&ms->pv_done[x][h]);
+        if (h) {
           mma_commit(&ms->kv_empty[vs]);
-          if (!v.s.pair) mma_commit(&ms->kv_empty[vs]);
+          if (!(f & kPairTile)) mma_commit(&ms->kv_empty[vs]);
         }
-        step(v);
-        return true;
       };
-      ok = issue_qk() && issue_qk();
-      while (ok) {
-        ok = settle(v, [] { return true; },
-                    [&] {
-                      used += v.jobs > 0;
-                      mbar_arrive(&ms->seg_empty[(v.nseg - 1) % NSEG]);
-                    });
-        if (!ok || v.over) break;
-        ok = issue_pv() && issue_qk();
+      // Q K^T of the tile after the current one between its P V, of either half
+      int T = 0, f = 0, n = 0, nT = -1, nf = 0;
+      if (find(T, f) && T >= 0) {
+        issue_qk(T, f, 0, 0);
+        issue_qk(T, f, 0, 1);
+        for (; ok && T >= 0; T = nT, f = nf, ++n) {
+          issue_pv(T, f, n, 0);
+          nT = T + 1;
+          if (ok) find(nT, nf);
+          if (ok && nT >= 0) issue_qk(nT, nf, n + 1, 0);
+          issue_pv(T, f, n, 1);
+          if (ok && nT >= 0) issue_qk(nT, nf, n + 1, 1);
+        }
       }
       if (!ok) {
         set_status(p.status, ETA_DEVSTAT_TIMEOUT);
@@ -928,8 +918,9 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
         const int T = s.base + tile_of(s, x, j);
         // V's slot is not loaded again before this tile's P V
         if (!wwait(&ms->s_full[x][0], (uint32_t)cnt & 1u) ||
-            !__all_sync(0xffffffffu, wait_load(&ms->kv_full[C::vslot(T)], C::vload(T),
-                                               &ms->issued, 2 * T + 1, abort_flag))) {
+            !__all_sync(0xffffffffu,
+                        wait_issued(&ms->issued, &ms->end, 2 * T + 1, abort_flag)) ||
+            !wwait(&ms->kv_full[C::vslot(T)], (uint32_t)C::vload(T) & 1u)) {
           ok = false;
           break;
         }
