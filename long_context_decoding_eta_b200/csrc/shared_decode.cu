@@ -41,8 +41,6 @@ namespace eta {
 namespace sd {
 
 using tc::fence_async_smem;
-using tc::mma_commit;
-using tc::mma_f16;
 using tc::smem_desc;
 using tc::tc_fence_after;
 using tc::tc_fence_before;
@@ -346,11 +344,37 @@ constexpr uint32_t idesc() {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-ETA_DEV void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
+// The MMA warps run with all their lanes, so that descriptors are computed in uniform
+// registers, and one elected lane issues: 8 MMAs take 229 cycles to issue this way, 546 from
+// a branch of one lane.
+ETA_DEV uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(e));
+  return e;
+}
+ETA_DEV void mma_ss(uint32_t lead, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id,
+                    uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(id), "r"(acc)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(id), "r"(acc), "r"(lead)
+      : "memory");
+}
+ETA_DEV void mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id,
+                    uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(id), "r"(acc), "r"(lead)
+      : "memory");
+}
+ETA_DEV void commit(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(
+          smem_u32(bar)),
+      "r"(lead)
       : "memory");
 }
 
@@ -772,17 +796,19 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
     // One warp for each stream, so that one stream's waits never hold up the other: Q K^T
     // once the stream's S columns (P of the job before) are free, P V once P is written.
     const int x = warp - 9;
-    if (lane == 0) {
-      bool ok = true;
+    {
+      const uint32_t lead = elect_one();
+      bool ok = true;                            // the same in all lanes, as all else
       const uint64_t dq = smem_desc(smem_u32(smem + C::OFF_Q), 16, 1024, tc::kSwizzle128);
       const uint64_t dk = smem_desc(smem_u32(smem + C::OFF_KV), 16, 1024, tc::kSwizzle128);
       const uint64_t dv = smem_desc(smem_u32(smem + C::OFF_KV), HALF, 1024, tc::kSwizzle128);
       const uint32_t tSx = tS[0] + x * 128, tOx = tO[0] + x * 128;
       constexpr uint32_t id = idesc<D>() | (1u << 16);           // V is MN-major
-      volatile int* issued = &ms->issued;
-      volatile int* end = &ms->end;
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return mbar_wait(bar, parity, abort_flag);
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+      };
+      auto is_issued = [&](int item) -> bool {
+        return __all_sync(0xffffffffu, wait_issued(&ms->issued, &ms->end, item, abort_flag));
       };
       // The stream's next tile, from T on, and its flags; T = -1: no more.  A barrier's
       // parity also looks over while the phase before is open, and a stream does not follow
@@ -791,17 +817,17 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
       // tile's K and V.
       auto find = [&](int& T, int& f) -> bool {
         for (;; ++T) {
-          if (!wait_issued(issued, end, 2 * T, abort_flag)) {
-            ok = *end <= T;
+          if (!is_issued(2 * T)) {
+            ok = __all_sync(0xffffffffu, *(volatile int*)&ms->end <= T);
             T = -1;
             return ok;
           }
-          f = *(volatile int*)&ms->tile[T % NTILE];
+          f = __shfl_sync(0xffffffffu, *(volatile int*)&ms->tile[T % NTILE], 0);
           if ((f & kPairTile) || (T & 1) == x) break;
         }
         if (f & kFirst) {
           const int qs = (f & kPairTile) ? x : (f & kQSlot) ? 1 : 0;
-          ok = wait_issued(issued, end, 2 * T + 1, abort_flag) &&
+          ok = is_issued(2 * T + 1) &&
                wait(&ms->q_full[qs], (f & (qs ? kQPhase1 : kQPhase0)) ? 1u : 0u);
         }
         return ok = ok && wait(&ms->kv_full[C::kslot(T)], (uint32_t)C::kload(T) & 1u);
@@ -818,15 +844,15 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t off = (uint64_t)(((kk >> 2) * HALF + (kk & 3) * 32) >> 4);
-          mma_f16(tSx + h * SUB, dqs + off, dks + off, idesc<SUB>(), kk > 0);
+          mma_ss(lead, tSx + h * SUB, dqs + off, dks + off, idesc<SUB>(), kk > 0);
         }
-        mma_commit(&ms->s_full[x][h]);
+        commit(lead, &ms->s_full[x][h]);
         if (h) {
           // a tile's slot is free after two arrivals: a pair's streams each give one
-          mma_commit(&ms->kv_empty[ks]);
-          if (!(f & kPairTile)) mma_commit(&ms->kv_empty[ks]);
-          if (f & (kQRel1 | kQRel2)) mma_commit(&ms->q_empty[qs]);
-          if (f & kQRel2) mma_commit(&ms->q_empty[qs]);
+          commit(lead, &ms->kv_empty[ks]);
+          if (!(f & kPairTile)) commit(lead, &ms->kv_empty[ks]);
+          if (f & (kQRel1 | kQRel2)) commit(lead, &ms->q_empty[qs]);
+          if (f & kQRel2) commit(lead, &ms->q_empty[qs]);
         }
       };
       int segs = 0;                              // segments begun
@@ -844,12 +870,12 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
         for (int term = 0; term < NS; ++term)
 #pragma unroll
           for (int kk = 0; kk < SUB / 16; ++kk)
-            mma_f16_ts(tOx, tSx + h * SUB + term * 32 + kk * 8, dvs + (uint64_t)(kk * 2048 >> 4),
+            mma_ts(lead, tOx, tSx + h * SUB + term * 32 + kk * 8, dvs + (uint64_t)(kk * 2048 >> 4),
                        id, (term > 0 || kk > 0) ? 1u : first ? 0u : 1u);
-        mma_commit(&ms->pv_done[x][h]);
+        commit(lead, &ms->pv_done[x][h]);
         if (h) {
-          mma_commit(&ms->kv_empty[vs]);
-          if (!(f & kPairTile)) mma_commit(&ms->kv_empty[vs]);
+          commit(lead, &ms->kv_empty[vs]);
+          if (!(f & kPairTile)) commit(lead, &ms->kv_empty[vs]);
         }
       };
       // Q K^T of the tile after the current one between its P V, of either half
@@ -867,12 +893,13 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
         }
       }
       if (!ok) {
-        set_status(p.status, ETA_DEVSTAT_TIMEOUT);
+        if (lead) set_status(p.status, ETA_DEVSTAT_TIMEOUT);
         *abort_flag = 1;
       }
       // every MMA issued so far has completed before TMEM is released
-      mma_commit(&ms->fin[x]);
+      commit(lead, &ms->fin[x]);
       mbar_wait(&ms->fin[x], 0, nullptr);
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------------ softmax
