@@ -1040,9 +1040,11 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
         tc_fence_after();
       }
       if (active) {
-        const int part = (x ? s.partB : s.partA) + i;
+        // O by 4 dims, the stream's `mine` rows side by side for each: a warp's stores
+        // coalesce (a row's own 512 bytes by each thread took 8,000 cycles a segment)
+        const int first = x ? s.partB : s.partA;
         const bool store = valid && (!s.check || p.ws.row[b].start > 0) &&
-                           ETA_IN_BOUNDS(part, p.part_rows, p.status);
+                           ETA_RANGE_IN_BOUNDS(first, first + mine, p.part_rows, p.status);
         if (jobs > 0) {
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
@@ -1050,15 +1052,17 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
             tmem_ld32(tOx + c * 32, ov);
             tmem_wait_ld32(ov);
             if (store) {
-              float4* to = reinterpret_cast<float4*>(p.ws.part_o + (size_t)part * D + c * 32);
+              float4* to = reinterpret_cast<float4*>(p.ws.part_o) + (size_t)first * (D / 4) +
+                           c * 8 * mine + i;
 #pragma unroll
               for (int u = 0; u < 8; ++u)
-                to[u] = make_float4(ov[4 * u], ov[4 * u + 1], ov[4 * u + 2], ov[4 * u + 3]);
+                to[u * mine] = make_float4(ov[4 * u], ov[4 * u + 1], ov[4 * u + 2], ov[4 * u + 3]);
             }
           }
         }
         if (store)
-          reinterpret_cast<float2*>(p.ws.part_ml)[part] = make_float2(m * p.scale, l2.x + l2.y);
+          reinterpret_cast<float2*>(p.ws.part_ml)[first + i] =
+              make_float2(m * p.scale, l2.x + l2.y);
       }
       tc_fence_before();
       __syncwarp();
@@ -1094,7 +1098,7 @@ ETA_DEV void store4(__nv_bfloat16* o, float4 v) {
 
 // One CTA per (row, KV head), its G heads together (their partial rows lie side by side).
 // The slots are the CTAs that had a piece of the row's prefix item (one or two streams
-// each) and of its own item.  Thread = (slot group, 4 dims of a head).
+// each) and of its own item.  Thread = (slot group, 4 dims, head).
 template <int D, int G, typename OutT>
 __global__ void __launch_bounds__(kCombine)
 shared_combine_kernel(const AttendParams p, OutT* __restrict__ o, float* __restrict__ lse) {
@@ -1107,14 +1111,19 @@ shared_combine_kernel(const AttendParams p, OutT* __restrict__ o, float* __restr
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Head hd = *p.ws.head;
   const RowRec r = p.ws.row[b];
-  int n1 = 0, first1 = 0, step1 = 0, two1 = 0, off1 = 0;    // prefix slots
+  // prefix slots: how many, their first, whether there are two a CTA, and where the row's
+  // heads lie in them
+  int n1 = 0, first1 = 0, step1 = 0, two1 = 0, off1 = 0, i1 = 0, rows1 = 0;
   if (r.group >= 0) {
     const GroupRec g = p.ws.grp[r.group];
     const int i = (b - g.row0) * G, pair = i / (2 * TILE), ii = i % (2 * TILE);
     const int item = kvh * g.npairs + pair, left = g.nrows * G - pair * 2 * TILE;
     const int a = g.off + item * g.nt * g.cost, c0 = a / hd.share;
     n1 = (a + (g.nt - 1) * g.cost) / hd.share - c0 + 1;
-    first1 = g.base + (c0 - g.cf + item) * g.rows + ii;
+    const int second = ii >= TILE ? TILE : 0;               // of a pair's query tiles
+    first1 = g.base + (c0 - g.cf + item) * g.rows + second;
+    i1 = ii - second;
+    rows1 = min(left - second, TILE);
     step1 = g.rows;
     two1 = left <= TILE;
     off1 = g.npairs == 1 ? left : TILE;
@@ -1126,12 +1135,13 @@ shared_combine_kernel(const AttendParams p, OutT* __restrict__ o, float* __restr
     first2 = hd.suffix_base + (c0 + b * p.Hkv + kvh) * 2 * G;
   }
   const int m1 = n1 * (1 + two1), n = min(m1 + 2 * n2, kMaxSlots);
-  auto slot = [&](int k) -> int {          // partial row of slot k's first head
+  auto slot = [&](int k) -> int {          // first row of slot k
     int s;
     if (k < m1) s = two1 ? first1 + (k >> 1) * step1 + (k & 1) * off1 : first1 + k * step1;
     else s = first2 + (k - m1) * G;
-    return ETA_RANGE_IN_BOUNDS(s, s + G, p.part_rows, p.status) ? s : 0;
+    return ETA_RANGE_IN_BOUNDS(s, s + (k < m1 ? rows1 : G), p.part_rows, p.status) ? s : 0;
   };
+  auto row_of = [&](int k) -> int { return slot(k) + (k < m1 ? i1 : 0); };
   // a thread's elements (slot, head) all have the head tid % G
   auto over_threads = [&](float v, auto op) -> float {
 #pragma unroll
@@ -1151,11 +1161,11 @@ shared_combine_kernel(const AttendParams p, OutT* __restrict__ o, float* __restr
 #pragma unroll
   for (int u = 0; u < KEEP; ++u) {
     const int x = tid + u * kCombine;
-    kept[u] = x < n * G ? ml[slot(x / G) + x % G] : make_float2(-INFINITY, 0.f);
+    kept[u] = x < n * G ? ml[row_of(x / G) + x % G] : make_float2(-INFINITY, 0.f);
     mx = fmaxf(mx, kept[u].x);
   }
   for (int x = tid + KEEP * kCombine; x < n * G; x += kCombine)
-    mx = fmaxf(mx, ml[slot(x / G) + x % G].x);
+    mx = fmaxf(mx, ml[row_of(x / G) + x % G].x);
   mx = over_threads(mx, [](float a, float c) { return fmaxf(a, c); });
   float l = 0.f;
   auto weigh = [&](int x, float2 v) {
@@ -1167,19 +1177,21 @@ shared_combine_kernel(const AttendParams p, OutT* __restrict__ o, float* __restr
   for (int u = 0; u < KEEP; ++u)
     if (tid + u * kCombine < n * G) weigh(tid + u * kCombine, kept[u]);
   for (int x = tid + KEEP * kCombine; x < n * G; x += kCombine)
-    weigh(x, ml[slot(x / G) + x % G]);
+    weigh(x, ml[row_of(x / G) + x % G]);
   l = over_threads(l, [](float a, float c) { return a + c; });
   const size_t head0 = (size_t)b * p.Hq + kvh * G;
   if (tid < G) {
     lse[head0 + tid] = l > 0.f ? mx + logf(l) : -INFINITY;
     red[0][tid] = l;
   }
-  const int v = tid % VEC, gi = tid / VEC, h = v / (D / 4);
+  // head fastest: the G heads of 4 dims are side by side in a slot
+  const int v = tid % VEC, gi = tid / VEC, h = v % G, vd = v / G;
   const float4* po = reinterpret_cast<const float4*>(p.ws.part_o);
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
   for (int k = gi; k < n; k += NG) {
-    const float4 x = po[(size_t)slot(k) * (D / 4) + v];
+    const float4 x = k < m1 ? po[(size_t)slot(k) * (D / 4) + vd * rows1 + i1 + h]
+                            : po[(size_t)slot(k) * (D / 4) + vd * G + h];
     const float e = w[k * G + h];
     if (e > 0.f) {                          // an empty slot's o was never written
       a.x = fmaf(e, x.x, a.x);
@@ -1208,7 +1220,7 @@ shared_combine_kernel(const AttendParams p, OutT* __restrict__ o, float* __restr
     } else {
       a = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    store4(o + head0 * D + v * 4, a);
+    store4(o + (head0 + h) * D + vd * 4, a);
   }
 }
 
