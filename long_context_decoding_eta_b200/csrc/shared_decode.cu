@@ -62,12 +62,19 @@ enum Gate { NONE = 0, HARD = 1, SOFT = 2 };
 // Costs in half microseconds, as measured (64 rows over 128K tokens, 4 KV heads): a key
 // tile of up to 256 or 128 queries, a key tile of a row's own, and what a row's own item
 // costs besides (its few tiles cannot fill the pipeline).  An item's tiles begin at 0 and
-// kSegCost + t * cost; a CTA has the tiles that begin in its share of the costs.
-constexpr int kPairCost = 4, kSingleCost = 3, kOwnCost = 3, kSegCost = 4;
-constexpr int kMinShare = kOwnCost + kSegCost;  // every share inside an item has a tile's begin
-static_assert(kMinShare >= kPairCost && kMinShare >= kSingleCost, "smallest share");
-ETA_DEV int own_begin(int t) { return t ? kSegCost + t * kOwnCost : 0; }
-ETA_DEV int own_cost(int nt) { return nt ? kSegCost + nt * kOwnCost : 0; }
+// seg + t * cost; a CTA has the tiles that begin in its share of the costs.  With few
+// tiles every tile costs 1, so that they spread over all CTAs: 4 rows of 2,048 + 64 tokens
+// are 80 tiles for 80 CTAs, where the costs above left 44 of them three each.
+struct Costs {
+  int pair, single, own, seg;
+  ETA_DEV int own_begin(int t) const { return t ? seg + t * own : 0; }
+  ETA_DEV int own_cost(int nt) const { return nt ? seg + nt * own : 0; }
+  // the smallest share: every share inside an item has a tile's begin
+  ETA_DEV int gap() const { return max(max(pair, single), own + seg); }
+};
+ETA_DEV Costs costs_of(int tiles, int P) {
+  return tiles <= 2 * P ? Costs{1, 1, 1, 0} : Costs{4, 3, 3, 4};
+}
 
 struct GroupRec {
   int off;        // its first item's place in the costs
@@ -91,6 +98,7 @@ struct RowRec {
 
 struct Head {
   int share, suffix_base;
+  Costs cost;
 };
 
 // What a CTA begins with: its share [a, e) of the costs, the group (or n_groups + row) at
@@ -142,6 +150,8 @@ ETA_DEV int2 cta_scan(int2 v, int2* wsum, int2& total) {   // exclusive, over kP
 __global__ void __launch_bounds__(kPlan) shared_plan_kernel(const PlanParams p) {
   ETA_PDL_ENTRY();
   __shared__ int2 wsum[32];
+  __shared__ int s_tiles;                       // of all items
+  if (threadIdx.x == 0) s_tiles = 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cap = p.NB * p.blk;
   bool bad = false;
@@ -186,9 +196,11 @@ __global__ void __launch_bounds__(kPlan) shared_plan_kernel(const PlanParams p) 
         }
     if (lane == 0) {
       GroupRec rec;
+      int tiles;
       const int rows = (r1 - r0) * p.G;
       rec.nt = share ? (nb * p.blk + TILE - 1) / TILE : 0;
-      rec.cost = rows > TILE ? kPairCost : kSingleCost;
+      rec.cost = rows > TILE;                    // pair or single: see below
+      tiles = p.Hkv * rec.nt * ((rows + 2 * TILE - 1) / (2 * TILE));
       rec.npairs = (rows + 2 * TILE - 1) / (2 * TILE);
       rec.row0 = r0;
       rec.nrows = r1 - r0;
@@ -197,31 +209,42 @@ __global__ void __launch_bounds__(kPlan) shared_plan_kernel(const PlanParams p) 
       rec.rows = rec.npairs > 1 ? 2 * TILE : rows <= TILE ? 2 * rows : rows;
       rec.off = rec.base = rec.cf = 0;
       p.ws.grp[g] = rec;
+      if (tiles) atomicAdd(&s_tiles, tiles);
     }
   }
   __syncthreads();
+  for (int b0 = 0; b0 < p.B; b0 += kPlan) {
+    const int b = b0 + threadIdx.x;
+    int nt = 0;
+    if (b < p.B) {
+      const int len = min(max(p.lengths[b], 0), cap);
+      nt = (max(len - p.ws.row[b].start * p.blk, 0) + TILE - 1) / TILE;
+      p.ws.row[b].nt = nt;
+    }
+    nt = __reduce_add_sync(0xffffffffu, nt);
+    if (lane == 0 && nt) atomicAdd(&s_tiles, nt * p.Hkv);
+  }
+  __syncthreads();
+  const Costs w = costs_of(s_tiles, p.P);
   // places in the costs: of the groups (x) and of the rows (y, counted from zero)
   int2 carry = make_int2(0, 0), total;
   for (int i0 = 0; i0 < max(p.n_groups, p.B); i0 += kPlan) {
     const int i = i0 + threadIdx.x;
     int2 n = make_int2(0, 0);
     if (i < p.n_groups) {
-      const GroupRec g = p.ws.grp[i];
+      GroupRec g = p.ws.grp[i];
+      g.cost = g.cost ? w.pair : w.single;
+      p.ws.grp[i].cost = g.cost;
       n.x = p.Hkv * g.npairs * g.nt * g.cost;
     }
-    if (i < p.B) {
-      const int len = min(max(p.lengths[i], 0), cap);
-      const int nt = (max(len - p.ws.row[i].start * p.blk, 0) + TILE - 1) / TILE;
-      p.ws.row[i].nt = nt;
-      n.y = p.Hkv * own_cost(nt);
-    }
+    if (i < p.B) n.y = p.Hkv * w.own_cost(p.ws.row[i].nt);
     const int2 off = add2(carry, cta_scan(n, wsum, total));
     if (i < p.n_groups) p.ws.grp[i].off = off.x;
     if (i < p.B) p.ws.row[i].off = off.y;
     carry = add2(carry, total);
   }
   const int prefix_cost = carry.x, costs = carry.x + carry.y;
-  const int share = max((costs + p.P - 1) / p.P, kMinShare);
+  const int share = max((costs + p.P - 1) / p.P, w.gap());
   for (int c = threadIdx.x; c < p.P; c += kPlan) {
     p.ws.cta[c].a = min(c * share, costs);
     p.ws.cta[c].e = min(c * share + share, costs);
@@ -256,11 +279,11 @@ __global__ void __launch_bounds__(kPlan) shared_plan_kernel(const PlanParams p) 
       p.ws.cta[c].item = g;
   }
   for (int b = threadIdx.x; b < p.B; b += kPlan) {
-    const int off = prefix_cost + p.ws.row[b].off, n = p.Hkv * own_cost(p.ws.row[b].nt);
+    const int off = prefix_cost + p.ws.row[b].off, n = p.Hkv * w.own_cost(p.ws.row[b].nt);
     for (int c = (off + share - 1) / share; c * share < off + n; ++c)
       p.ws.cta[c].item = p.n_groups + b;
   }
-  if (threadIdx.x == 0) *p.ws.head = Head{share, carry.x};
+  if (threadIdx.x == 0) *p.ws.head = Head{share, carry.x, w};
 }
 
 // ---------------------------------------------------------------------------- attend
@@ -570,7 +593,9 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
     // The whole warp: 32 pages are looked up at a time, a tile's boxes are issued by a
     // lane each.  Every variable but the lane's own page and box is the same in all lanes.
     const CtaRec me = p.ws.cta[blockIdx.x];
-    const int suffix_base = p.ws.head->suffix_base;
+    const Head hd = *p.ws.head;
+    const int suffix_base = hd.suffix_base;
+    const Costs w = hd.cost;
     const int e = me.e, shift = p.blk == 64 ? 6 : 7;
     int pos = me.a, at = me.item;
     bool ok = true;
@@ -647,7 +672,7 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
           pg_row = page_of(b, r.start << shift, len);
         }
         int local = pos - me.prefix_cost - r.off;
-        if (local >= own_cost(r.nt) * p.Hkv) {
+        if (local >= w.own_cost(r.nt) * p.Hkv) {
           if (b + 1 >= p.B) {                    // cannot happen: a place has an item
             pos = e;
             break;
@@ -661,12 +686,12 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
           next_row();
           continue;
         }
-        const int ic = own_cost(r.nt), g = local / ic, base = pos - local + g * ic;
+        const int ic = w.own_cost(r.nt), g = local / ic, base = pos - local + g * ic;
         local -= g * ic;
         // the first tile that begins at pos or behind it, and the first behind the share
-        const int t = local == 0 ? 0 : max((local - kSegCost + kOwnCost - 1) / kOwnCost, 1);
-        const int te = min(max((e - base - kSegCost + kOwnCost - 1) / kOwnCost, 1), r.nt);
-        pos = base + (t >= r.nt ? ic : own_begin(t));
+        const int t = local == 0 ? 0 : max((local - w.seg + w.own - 1) / w.own, 1);
+        const int te = min(max((e - base - w.seg + w.own - 1) / w.own, 1), r.nt);
+        pos = base + (t >= r.nt ? ic : w.own_begin(t));
         if (t >= r.nt || pos >= e) continue;
         s.live = 1;
         s.pair = 0;
@@ -681,7 +706,7 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
         trow = b;
         mrows = p.G;
         pg = t == 0 ? pg_row : page_of(b, key0, len);
-        pos = base + (te == r.nt ? ic : own_begin(te));
+        pos = base + (te == r.nt ? ic : w.own_begin(te));
       }
       s.base = slots / 2;
       // Tile T of single segments is stream T & 1's, so that a stream's next tile is never
@@ -924,6 +949,7 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
       const int b = s.row0 + (i + (s.pair && x ? TILE : 0)) / p.G, h = s.kvh * p.G + i % p.G;
       const bool valid = i < mine && ETA_IN_BOUNDS(b, p.B, p.status) &&
                          ETA_IN_BOUNDS(h, p.Hq, p.status);
+      const bool store = valid && (!s.check || p.ws.row[b].start > 0);   // the row shares
       // Gated logits in raw units u (the gated logit is scale * u), so that the scale
       // folds into the constants: the hard gate keeps s iff s >= tau / scale; the soft
       // gate is hs + hs * tanh(s * ta - tb), hs = s / 2, for a bf16 output (one
@@ -1043,15 +1069,14 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
         // O by 4 dims, the stream's `mine` rows side by side for each: a warp's stores
         // coalesce (a row's own 512 bytes by each thread took 8,000 cycles a segment)
         const int first = x ? s.partB : s.partA;
-        const bool store = valid && (!s.check || p.ws.row[b].start > 0) &&
-                           ETA_RANGE_IN_BOUNDS(first, first + mine, p.part_rows, p.status);
+        const bool in = ETA_RANGE_IN_BOUNDS(first, first + mine, p.part_rows, p.status);
         if (jobs > 0) {
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             float ov[32];
             tmem_ld32(tOx + c * 32, ov);
             tmem_wait_ld32(ov);
-            if (store) {
+            if (store && in) {
               float4* to = reinterpret_cast<float4*>(p.ws.part_o) + (size_t)first * (D / 4) +
                            c * 8 * mine + i;
 #pragma unroll
@@ -1060,7 +1085,7 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
             }
           }
         }
-        if (store)
+        if (store && in)
           reinterpret_cast<float2*>(p.ws.part_ml)[first + i] =
               make_float2(m * p.scale, l2.x + l2.y);
       }
@@ -1130,8 +1155,8 @@ shared_combine_kernel(const AttendParams p, OutT* __restrict__ o, float* __restr
   }
   int n2 = 0, first2 = 0;                                   // the row's own slots
   if (r.nt > 0) {
-    const int a = p.ws.cta[0].prefix_cost + r.off + kvh * own_cost(r.nt), c0 = a / hd.share;
-    n2 = (a + own_begin(r.nt - 1)) / hd.share - c0 + 1;
+    const int a = p.ws.cta[0].prefix_cost + r.off + kvh * hd.cost.own_cost(r.nt), c0 = a / hd.share;
+    n2 = (a + hd.cost.own_begin(r.nt - 1)) / hd.share - c0 + 1;
     first2 = hd.suffix_base + (c0 + b * p.Hkv + kvh) * 2 * G;
   }
   const int m1 = n1 * (1 + two1), n = min(m1 + 2 * n2, kMaxSlots);
