@@ -468,15 +468,32 @@ ETA_DEV void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
       : "memory");
 }
 
+// A whole warp's wait.  What is inlined is one try (which itself waits a while); the polls
+// behind it are out of line, since the roles of a CTA share the instruction caches.
+__noinline__ __device__ bool warp_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+ETA_DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
+         warp_wait_slow(bar, parity, abort);
+}
+
 // Waits until load `item` (tile T's K is 2 T, its V 2 T + 1) has been issued; false too
-// when the CTA has no such tile.
+// when the CTA has no such tile.  A whole warp's wait.
+__noinline__ __device__ bool wait_issued_slow(volatile int* issued, volatile int* end, int item,
+                                              volatile int* abort) {
+  uint32_t polls = 0;
+  bool ok = true;
+  while (ok && *issued <= item)
+    ok = !(*end <= item / 2 || ++polls > kIssueLimit || *abort);
+  return __all_sync(0xffffffffu, ok);
+}
 ETA_DEV bool wait_issued(volatile int* issued, volatile int* end, int item,
                          volatile int* abort) {
-  uint32_t polls = 0;
-  while (*issued <= item)
-    if (*end <= item / 2 || ++polls > kIssueLimit || *abort) return false;
+  const bool ok = __all_sync(0xffffffffu, *issued > item) ||
+                  wait_issued_slow(issued, end, item, abort);
   __threadfence_block();
-  return true;
+  return ok;
 }
 
 // The gate on 32 scores of a query row, in raw units (see the softmax).
@@ -624,7 +641,7 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
     };
     // every lane polls; all agree on the outcome
     auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+      return warp_wait(bar, parity, abort_flag);
     };
     while (ok) {
       Seg s = {};
@@ -830,10 +847,10 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
       const uint32_t tSx = tS[0] + x * 128, tOx = tO[0] + x * 128;
       constexpr uint32_t id = idesc<D>() | (1u << 16);           // V is MN-major
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+        return warp_wait(bar, parity, abort_flag);
       };
       auto is_issued = [&](int item) -> bool {
-        return __all_sync(0xffffffffu, wait_issued(&ms->issued, &ms->end, item, abort_flag));
+        return wait_issued(&ms->issued, &ms->end, item, abort_flag);
       };
       // The stream's next tile, from T on, and its flags; T = -1: no more.  A barrier's
       // parity also looks over while the phase before is open, and a stream does not follow
@@ -937,7 +954,7 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
     bool ok = true;
     int nseg = 0, cnt = 0;
     auto wwait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+      return warp_wait(bar, parity, abort_flag);
     };
     for (;; ++nseg) {
       const int sl = nseg % NSEG;
@@ -971,8 +988,7 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
         const int T = s.base + tile_of(s, x, j);
         // V's slot is not loaded again before this tile's P V
         if (!wwait(&ms->s_full[x][0], (uint32_t)cnt & 1u) ||
-            !__all_sync(0xffffffffu,
-                        wait_issued(&ms->issued, &ms->end, 2 * T + 1, abort_flag)) ||
+            !wait_issued(&ms->issued, &ms->end, 2 * T + 1, abort_flag) ||
             !wwait(&ms->kv_full[C::vslot(T)], (uint32_t)C::vload(T) & 1u)) {
           ok = false;
           break;
