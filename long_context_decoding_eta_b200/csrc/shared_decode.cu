@@ -15,8 +15,9 @@
 //                        (row, head) pairs) over the prefix, or (row, KV head) over the
 //                        row's own keys, in key tiles of 128.  The items' costs, laid end
 //                        to end, are cut into equal shares, one per SM.
-//   shared_attend_kernel one CTA per share: 352 threads, warps 0-3 / 4-7 the softmax of
-//                        streams A / B, warp 8 the TMA producer, warps 9 / 10 their MMAs.
+//   shared_attend_kernel one CTA per share: 384 threads, warps 0-3 / 4-7 the softmax of
+//                        streams A / B, warp 8 the TMA producer, warps 9 / 10 their Q K^T,
+//                        warp 11 the P V of both.
 //                        S_x = Q K^T and O_x += P V with M = 128 queries, N = 128 keys;
 //                        a thread owns a query row, so no row statistic is exchanged.
 //                        Two streams keep the tensor cores busy while the other stream's
@@ -50,7 +51,7 @@ constexpr int TILE = 128;                       // query rows and keys of a tile
 constexpr int SUB = 64;                         // keys of a TMA box (half a tile)
 constexpr int HALF = TILE * 128;                // [128 rows x 64 dims] bf16 = 16 KB
 constexpr int NSEG = 4;                         // segment records in flight
-constexpr int NT = 352;
+constexpr int NT = 384;
 constexpr int kPlan = 1024;
 constexpr int kTmemCols = 512;
 constexpr uint32_t kIssueLimit = 1u << 26;      // polls for a load to be issued
@@ -322,7 +323,7 @@ struct Misc {
   static constexpr int NSLOT = D == 128 ? 5 : 10;
   uint64_t q_full[2], q_empty[2], kv_full[NSLOT], kv_empty[NSLOT];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], o_free[2];   // [stream][half tile]
-  uint64_t seg_full[NSEG], seg_empty[NSEG], fin[2];
+  uint64_t seg_full[NSEG], seg_empty[NSEG], fin[3];
   Seg seg[NSEG];
   int2 nv[NSLOT];       // of a V slot: valid keys of the tile's two 64-key halves
   int tile[NTILE];      // TileFlags
@@ -429,6 +430,16 @@ ETA_DEV void tmem_st32(uint32_t taddr, const uint32_t* v) {
       : "memory");
 }
 
+ETA_DEV void tmem_st16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+      "r"(v[15])
+      : "memory");
+}
+
 // Waits for the thread's loads; the 32 values are operands so that their use stays behind.
 ETA_DEV void tmem_wait_ld32(float* v) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -468,9 +479,22 @@ ETA_DEV void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
       : "memory");
 }
 
+// Whether phase `parity` of `bar` is over, without waiting.
+ETA_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // A whole warp's wait.  What is inlined is one try (which itself waits a while); the polls
 // behind it are out of line, since the roles of a CTA share the instruction caches.
-__noinline__ __device__ bool warp_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort) {
+ETA_DEV bool warp_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
 }
 ETA_DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
@@ -480,7 +504,7 @@ ETA_DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
 
 // Waits until load `item` (tile T's K is 2 T, its V 2 T + 1) has been issued; false too
 // when the CTA has no such tile.  A whole warp's wait.
-__noinline__ __device__ bool wait_issued_slow(volatile int* issued, volatile int* end, int item,
+ETA_DEV bool wait_issued_slow(volatile int* issued, volatile int* end, int item,
                                               volatile int* abort) {
   uint32_t polls = 0;
   bool ok = true;
@@ -587,6 +611,7 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
       mbar_init(&ms->seg_full[s], 1);
       mbar_init(&ms->seg_empty[s], 8);          // the softmax warps
     }
+    mbar_init(&ms->fin[2], 1);
     ms->issued = 0;
     ms->end = 0x7fffffff;
     ms->abort_flag = 0;
@@ -835,16 +860,16 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
     __syncwarp();
   } else if (warp > 8) {
     // ------------------------------------------------------------------ MMA issuers
-    // One warp for each stream, so that one stream's waits never hold up the other: Q K^T
-    // once the stream's S columns (P of the job before) are free, P V once P is written.
-    const int x = warp - 9;
+    // A warp for each stream's Q K^T, which is issued once the stream's S columns (P of the
+    // tile before) are free, and one for the P V of both streams, whichever has its P
+    // written.  (13 warps leave 128 registers a thread, and the softmax spilled: 161 us for
+    // 104 with one warp a stream for both products, 64 rows of 128K tokens.)
     {
       const uint32_t lead = elect_one();
       bool ok = true;                            // the same in all lanes, as all else
       const uint64_t dq = smem_desc(smem_u32(smem + C::OFF_Q), 16, 1024, tc::kSwizzle128);
       const uint64_t dk = smem_desc(smem_u32(smem + C::OFF_KV), 16, 1024, tc::kSwizzle128);
       const uint64_t dv = smem_desc(smem_u32(smem + C::OFF_KV), HALF, 1024, tc::kSwizzle128);
-      const uint32_t tSx = tS[0] + x * 128, tOx = tO[0] + x * 128;
       constexpr uint32_t id = idesc<D>() | (1u << 16);           // V is MN-major
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
         return warp_wait(bar, parity, abort_flag);
@@ -852,21 +877,15 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
       auto is_issued = [&](int item) -> bool {
         return wait_issued(&ms->issued, &ms->end, item, abort_flag);
       };
-      // The stream's next tile, from T on, and its flags; T = -1: no more.  A barrier's
-      // parity also looks over while the phase before is open, and a stream does not follow
-      // the loads of the other's tiles: that a load has been issued says that those before
-      // it into the same slot are over.  The queries' load is issued between the first
-      // tile's K and V.
-      auto find = [&](int& T, int& f) -> bool {
-        for (;; ++T) {
-          if (!is_issued(2 * T)) {
-            ok = __all_sync(0xffffffffu, *(volatile int*)&ms->end <= T);
-            T = -1;
-            return ok;
-          }
-          f = __shfl_sync(0xffffffffu, *(volatile int*)&ms->tile[T % NTILE], 0);
-          if ((f & kPairTile) || (T & 1) == x) break;
-        }
+      // The flags of tile T.  A barrier's parity also looks over while the phase before is
+      // open, and a stream does not follow the loads of the other's tiles: that a load has
+      // been issued says that those before it into the same slot are over.  The queries'
+      // load is issued between the first tile's K and V.
+      auto flags = [&](int T) -> int {
+        return __shfl_sync(0xffffffffu, *(volatile int*)&ms->tile[T % NTILE], 0);
+      };
+      // Q and K of a tile are in
+      auto ready = [&](int x, int T, int f) -> bool {
         if (f & kFirst) {
           const int qs = (f & kPairTile) ? x : (f & kQSlot) ? 1 : 0;
           ok = is_issued(2 * T + 1) &&
@@ -875,7 +894,7 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
         return ok = ok && wait(&ms->kv_full[C::kslot(T)], (uint32_t)C::kload(T) & 1u);
       };
       // S_h = Q K_h^T of tile T, the stream's n-th
-      auto issue_qk = [&](int T, int f, int n, int h) {
+      auto issue_qk = [&](int x, int T, int f, int n, int h) {
         // S_h's columns hold P of the tile before until P V has read it
         if (ok && n > 0) ok = wait(&ms->pv_done[x][h], (uint32_t)(n - 1) & 1u);
         if (!ok) return;
@@ -886,7 +905,7 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t off = (uint64_t)(((kk >> 2) * HALF + (kk & 3) * 32) >> 4);
-          mma_ss(lead, tSx + h * SUB, dqs + off, dks + off, idesc<SUB>(), kk > 0);
+          mma_ss(lead, tmem + x * 128 + h * SUB, dqs + off, dks + off, idesc<SUB>(), kk > 0);
         }
         commit(lead, &ms->s_full[x][h]);
         if (h) {
@@ -897,50 +916,92 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
           if (f & kQRel2) commit(lead, &ms->q_empty[qs]);
         }
       };
-      int segs = 0;                              // segments begun
-      // O += P_h V_h of tile T, the stream's n-th (V is in: the softmax waited for it)
-      auto issue_pv = [&](int T, int f, int n, int h) {
-        const bool first = h == 0 && (f & kFirst);
-        // the stream's last segment has to be read out of O before O begins anew
-        if (ok && first && segs++ > 0) ok = wait(&ms->o_free[x], (uint32_t)segs & 1u);
-        if (ok) ok = wait(&ms->p_full[x][h], (uint32_t)n & 1u);
+      // O += P_h V_h of tile T of stream x (V is in: the softmax waited for it)
+      auto issue_pv = [&](int x, int T, int f, int h) {
         const int vs = C::vslot(T);
-        if (!ok || !(ok = wait(&ms->kv_full[vs], (uint32_t)C::vload(T) & 1u))) return;
+        if (!(ok = wait(&ms->kv_full[vs], (uint32_t)C::vload(T) & 1u))) return;
         tc_fence_after();
         const uint64_t dvs = dv + (uint64_t)(vs * (C::SLOT >> 4) + h * (HALF / 2 >> 4));
+        const uint32_t acc = h == 0 && (f & kFirst) ? 0u : 1u;
 #pragma unroll
         for (int term = 0; term < NS; ++term)
 #pragma unroll
           for (int kk = 0; kk < SUB / 16; ++kk)
-            mma_ts(lead, tOx, tSx + h * SUB + term * 32 + kk * 8, dvs + (uint64_t)(kk * 2048 >> 4),
-                       id, (term > 0 || kk > 0) ? 1u : first ? 0u : 1u);
+            mma_ts(lead, tmem + 256 + x * 128, tmem + x * 128 + h * SUB + term * 32 + kk * 8,
+                   dvs + (uint64_t)(kk * 2048 >> 4), id, (term > 0 || kk > 0) ? 1u : acc);
         commit(lead, &ms->pv_done[x][h]);
         if (h) {
           commit(lead, &ms->kv_empty[vs]);
           if (!(f & kPairTile)) commit(lead, &ms->kv_empty[vs]);
         }
       };
-      // Q K^T of the tile after the current one between its P V, of either half
-      int T = 0, f = 0, n = 0, nT = -1, nf = 0;
-      if (find(T, f) && T >= 0) {
-        issue_qk(T, f, 0, 0);
-        issue_qk(T, f, 0, 1);
-        for (; ok && T >= 0; T = nT, f = nf, ++n) {
-          issue_pv(T, f, n, 0);
-          nT = T + 1;
-          if (ok) find(nT, nf);
-          if (ok && nT >= 0) issue_qk(nT, nf, n + 1, 0);
-          issue_pv(T, f, n, 1);
-          if (ok && nT >= 0) issue_qk(nT, nf, n + 1, 1);
+      if (warp < 11) {
+        const int x = warp - 9;
+        for (int T = 0, n = 0; ok; ++T) {
+          if (!is_issued(2 * T)) {
+            ok = __all_sync(0xffffffffu, *(volatile int*)&ms->end <= T);
+            break;
+          }
+          const int f = flags(T);
+          if (!(f & kPairTile) && (T & 1) != x) continue;
+          if (!ready(x, T, f)) break;
+          issue_qk(x, T, f, n, 0);
+          issue_qk(x, T, f, n, 1);
+          ++n;
         }
+      } else {
+        // per stream: its tile (have), the tile's half, tiles so far, segments begun
+        int T[2] = {0, 0}, f[2] = {0, 0}, h[2] = {0, 0}, n[2] = {0, 0}, segs[2] = {0, 0};
+        bool have[2] = {false, false}, over[2] = {false, false};
+        auto seen = [&](uint64_t* bar, uint32_t parity) -> bool {
+          return __all_sync(0xffffffffu, mbar_test(bar, parity));
+        };
+        uint32_t idle = 0;
+        while (ok && !(over[0] && over[1])) {
+          bool did = false;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (over[x] || !ok) continue;
+            if (!have[x]) {
+              if (!__all_sync(0xffffffffu, *(volatile int*)&ms->issued > 2 * T[x])) {
+                over[x] = __all_sync(0xffffffffu, *(volatile int*)&ms->end <= T[x]);
+                continue;
+              }
+              __threadfence_block();
+              f[x] = flags(T[x]);
+              did = true;
+              if (!(f[x] & kPairTile) && (T[x] & 1) != x) {
+                ++T[x];
+                continue;
+              }
+              have[x] = true;
+            }
+            // the stream's last segment has to be read out of O before O begins anew
+            if (h[x] == 0 && (f[x] & kFirst) && segs[x] > 0 &&
+                !seen(&ms->o_free[x], (uint32_t)(segs[x] - 1) & 1u))
+              continue;
+            if (!seen(&ms->p_full[x][h[x]], (uint32_t)n[x] & 1u)) continue;
+            did = true;
+            if (h[x] == 0 && (f[x] & kFirst)) ++segs[x];
+            issue_pv(x, T[x], f[x], h[x]);
+            if ((h[x] ^= 1) == 0) {
+              have[x] = false;
+              ++T[x];
+              ++n[x];
+            }
+          }
+          idle = did ? 0 : idle + 1;
+          if (idle > kIssueLimit || *abort_flag) ok = false;
+        }
+        ok = __all_sync(0xffffffffu, ok);
       }
       if (!ok) {
         if (lead) set_status(p.status, ETA_DEVSTAT_TIMEOUT);
         *abort_flag = 1;
       }
       // every MMA issued so far has completed before TMEM is released
-      commit(lead, &ms->fin[x]);
-      mbar_wait(&ms->fin[x], 0, nullptr);
+      commit(lead, &ms->fin[warp - 9]);
+      mbar_wait(&ms->fin[warp - 9], 0, nullptr);
       __syncwarp();
     }
   } else {
@@ -1062,11 +1123,13 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
               l2.y *= alpha;
             }
             const float nm = m == -INFINITY ? 0.f : -m * c1;
-            uint32_t hi[32], lo[NS == 2 ? 32 : 1];
-            exp32<NS>(sv, c1, nm, l2, hi, lo);
-            exp32<NS>(sv + 32, c1, nm, l2, hi + 16, NS == 2 ? lo + 16 : lo);
-            tmem_st32(tSh, hi);
-            if constexpr (NS == 2) tmem_st32(tSh + 32, lo);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t hi[16], lo[16];
+              exp32<NS>(sv + 32 * c, c1, nm, l2, hi, lo);
+              tmem_st16(tSh + 16 * c, hi);
+              if constexpr (NS == 2) tmem_st16(tSh + 32 + 16 * c, lo);
+            }
             tmem_wait_st();
           }
           tc_fence_before();
