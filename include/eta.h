@@ -580,7 +580,9 @@ typedef enum { ETA_OUT_F32 = 0, ETA_OUT_BF16 = 1 } eta_out_format_t;
  *                    else the blocks union_idx[b, g, 0 .. union_cnt[b, g])
  * o: fp32 or bf16 [B, Hq, d] by o_format; lse fp32 [B, Hq].  The other arguments as
  * eta_decode (prune, vsum and cnt included).  Always the tensor-core engine
- * (eta_set_decode_engine does not apply).  ws: eta_decode_workspace_size(dims) bytes.
+ * (eta_set_decode_engine does not apply), with the weights as the sum of two bf16 terms
+ * (2^-16) for a bf16 output and of three (2^-24) for an fp32 one.
+ * ws: eta_decode_workspace_size(dims) bytes.
  * dev_status: TIMEOUT, BAD_LENGTH, BAD_BLOCK (a block past the row's length, or a page
  * out of range: skipped).
  */
@@ -606,11 +608,13 @@ eta_status_t eta_paged_decode(const eta_dims_t* dims, int32_t n_pages, const eta
  * prefix come from the group's first row that is long enough: a row of the group whose
  * table holds other pages there gets the group's keys, not its own.  Rows of length 0
  * give o = 0, lse = -inf.
- * The prefix of up to 256 (row, head) pairs of one KV head is one pass of 128 x 128
- * tensor-core tiles (S = Q K^T, O += P V) over its keys, cut into equal shares of key
- * tiles, one per SM; the rows' own keys are shares of the same kind.  bf16 output: the
- * weights P are rounded to bf16 (a relative error of at most 2^-8, the output's own);
- * fp32 output: P is the sum of two bf16 terms (2^-16).
+ * The prefix of up to 256 (row, head) pairs of one KV head is one pass of tensor-core
+ * tiles (S = Q K^T, O += P V, 128 keys each) over its keys; a row's own keys are a pass
+ * of their own; all passes are cut into shares of equal cost, one per SM.  bf16 output:
+ * the weights P are rounded to bf16 (a relative error of at most 2^-8, the output's own)
+ * and the soft gate takes an approximate tanh (2^-11); fp32 output: P is the sum of
+ * three bf16 terms (2^-24) and the gate an exponential and a division.
+ * scale > 0 (0: 1 / sqrt(d)).
  * table, lengths, o_format, o, lse: as eta_paged_decode.
  * ws: eta_shared_decode_workspace_size(dims, n_groups) bytes, 16-byte aligned, no
  * initial contents.  1 <= n_groups <= B.

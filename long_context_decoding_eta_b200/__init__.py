@@ -8,11 +8,11 @@ does, and fails loudly if it has not been built.
 """
 from . import synth  # noqa: F401  (seeded input generator, no method arithmetic)
 
-__all__ = ["synth", "api", "_lib"]
+__all__ = ["synth", "api", "paged", "_lib"]
 
 
 def __getattr__(name):
-    if name in ("api", "_lib"):
+    if name in ("api", "paged", "_lib"):
         import importlib
         return importlib.import_module(f".{name}", __name__)
     raise AttributeError(name)

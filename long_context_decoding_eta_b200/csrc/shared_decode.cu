@@ -18,13 +18,15 @@
 //   shared_attend_kernel one CTA per share: 384 threads, warps 0-3 / 4-7 the softmax of
 //                        streams A / B, warp 8 the TMA producer, warps 9 / 10 their Q K^T,
 //                        warp 11 the P V of both.
-//                        S_x = Q K^T and O_x += P V with M = 128 queries, N = 128 keys;
-//                        a thread owns a query row, so no row statistic is exchanged.
+//                        S_x = Q K^T and O_x += P V with M = 128 queries, 64 keys at a
+//                        time: one half of a key tile is in the softmax while the other's
+//                        products run.  A thread owns a query row, so no row statistic is
+//                        exchanged.
 //                        Two streams keep the tensor cores busy while the other stream's
 //                        exponentials run: with more than 128 pairs A and B are two query
 //                        tiles that share every K/V tile; else they take alternate K/V
 //                        tiles of the one query tile, with accumulators of their own.
-//                        TMEM: S_A S_B O_A O_B, 128 columns each; P overwrites S.
+//                        P overwrites S in tensor memory.
 //   shared_combine_kernel  joins the parts of every (row, head).
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -527,16 +529,9 @@ struct GateArgs {
 template <int GATE, int NS>
 ETA_DEV void gate32(float* v, const GateArgs& g) {
   if constexpr (GATE == HARD) {
-    // a 1.0 / 0.0 flag and one packed multiply for two scores
+    // a selection: a flag times the score would make NaN of an infinite score
 #pragma unroll
-    for (int u = 0; u < 32; u += 2) {
-      float f0, f1;
-      asm("set.ge.f32.f32 %0, %1, %2;" : "=f"(f0) : "f"(v[u]), "f"(g.tau_raw));
-      asm("set.ge.f32.f32 %0, %1, %2;" : "=f"(f1) : "f"(v[u + 1]), "f"(g.tau_raw));
-      const float2 y = __fmul2_rn(make_float2(v[u], v[u + 1]), make_float2(f0, f1));
-      v[u] = y.x;
-      v[u + 1] = y.y;
-    }
+    for (int u = 0; u < 32; ++u) v[u] = v[u] >= g.tau_raw ? v[u] : 0.f;
   } else if constexpr (GATE == SOFT) {
 #pragma unroll
     for (int u = 0; u < 32; ++u) {
@@ -557,26 +552,42 @@ ETA_DEV void max32(const float* v, float* pm) {
 }
 
 // 32 weights e^(scale * (u - m)) = 2^(u * c1 + nm), summed into l2 and rounded to NS
-// bf16 terms, two keys a register.
+// bf16 terms (each the rounding of what those before it leave), two keys a register.
 template <int NS>
-ETA_DEV void exp32(const float* v, float c1, float nm, float2& l2, uint32_t* hi, uint32_t* lo) {
+ETA_DEV void exp32(const float* v, float c1, float nm, float2& l2, uint32_t (&w)[NS][16]) {
 #pragma unroll
   for (int u = 0; u < 16; ++u) {
     const float2 a = __ffma2_rn(make_float2(v[2 * u], v[2 * u + 1]), make_float2(c1, c1),
                                 make_float2(nm, nm));
-    const float2 pr = make_float2(ex2_approx(a.x), ex2_approx(a.y));
-    l2 = __fadd2_rn(l2, pr);
-    const __nv_bfloat162 hb = __floats2bfloat162_rn(pr.x, pr.y);
-    hi[u] = *reinterpret_cast<const uint32_t*>(&hb);
-    if constexpr (NS == 2) {
-      const float2 f = __bfloat1622float2(hb);
-      const __nv_bfloat162 lb = __floats2bfloat162_rn(pr.x - f.x, pr.y - f.y);
-      lo[u] = *reinterpret_cast<const uint32_t*>(&lb);
+    float2 r = make_float2(ex2_approx(a.x), ex2_approx(a.y));
+    l2 = __fadd2_rn(l2, r);
+#pragma unroll
+    for (int k = 0; k < NS; ++k) {
+      const __nv_bfloat162 t = __floats2bfloat162_rn(r.x, r.y);
+      w[k][u] = *reinterpret_cast<const uint32_t*>(&t);
+      const float2 f = __bfloat1622float2(t);
+      r.x -= f.x;
+      r.y -= f.y;
     }
   }
 }
 
-// GATE: Gate.  NS: the bf16 terms of P (1: bf16 output, 2: fp32 output).
+// Tensor-memory columns: stream x's scores of half h at x * S_STREAM + h * S_HALF, P over
+// them in NS terms of 32 columns; O behind.  Three terms take 96 columns: at d = 128, where
+// O needs half of tensor memory, the two halves of a stream then share theirs and take
+// turns.
+template <int D, int NS>
+struct Tm {
+  static constexpr int S_STREAM = D == 64 ? 192 : 128;
+  static constexpr int S_HALF = D == 64 ? 96 : NS == 1 ? 64 : 0;
+  static constexpr int O = 2 * S_STREAM, O_STREAM = D;
+  static_assert(O + 2 * O_STREAM <= kTmemCols, "tensor memory");
+  static_assert(NS * 32 <= (S_HALF ? S_HALF : S_STREAM), "P terms");
+};
+
+// GATE: Gate.  NS: the bf16 terms of P.  One (2^-9) for a bf16 output, whose own rounding
+// is the same; three (2^-27) for an fp32 one, where two (2^-18) left an error of 2e-6, eight
+// times the plain fp32 form's.
 template <int D, int GATE, int NS>
 __global__ void __launch_bounds__(NT, 1)
 shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -627,7 +638,7 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms->tmem_base;
-  const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 384};
+  using M = Tm<D, NS>;
   ETA_PDL_ENTRY();
 
   if (warp == 8) {
@@ -895,8 +906,12 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
       };
       // S_h = Q K_h^T of tile T, the stream's n-th
       auto issue_qk = [&](int x, int T, int f, int n, int h) {
-        // S_h's columns hold P of the tile before until P V has read it
-        if (ok && n > 0) ok = wait(&ms->pv_done[x][h], (uint32_t)(n - 1) & 1u);
+        // S_h's columns hold P of the tile before until P V has read it; or of the half before
+        if (M::S_HALF == 0 && h == 1) {
+          if (ok) ok = wait(&ms->pv_done[x][0], (uint32_t)n & 1u);
+        } else if (ok && n > 0) {
+          ok = wait(&ms->pv_done[x][M::S_HALF == 0 ? 1 : h], (uint32_t)(n - 1) & 1u);
+        }
         if (!ok) return;
         tc_fence_after();
         const int ks = C::kslot(T), qs = (f & kPairTile) ? x : (f & kQSlot) ? 1 : 0;
@@ -905,7 +920,7 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t off = (uint64_t)(((kk >> 2) * HALF + (kk & 3) * 32) >> 4);
-          mma_ss(lead, tmem + x * 128 + h * SUB, dqs + off, dks + off, idesc<SUB>(), kk > 0);
+          mma_ss(lead, tmem + x * M::S_STREAM + h * M::S_HALF, dqs + off, dks + off, idesc<SUB>(), kk > 0);
         }
         commit(lead, &ms->s_full[x][h]);
         if (h) {
@@ -927,8 +942,8 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
         for (int term = 0; term < NS; ++term)
 #pragma unroll
           for (int kk = 0; kk < SUB / 16; ++kk)
-            mma_ts(lead, tmem + 256 + x * 128, tmem + x * 128 + h * SUB + term * 32 + kk * 8,
-                   dvs + (uint64_t)(kk * 2048 >> 4), id, (term > 0 || kk > 0) ? 1u : acc);
+            mma_ts(lead, tmem + M::O + x * M::O_STREAM,
+                   tmem + x * M::S_STREAM + h * M::S_HALF + term * 32 + kk * 8, dvs + (uint64_t)(kk * 2048 >> 4), id, (term > 0 || kk > 0) ? 1u : acc);
         commit(lead, &ms->pv_done[x][h]);
         if (h) {
           commit(lead, &ms->kv_empty[vs]);
@@ -1009,7 +1024,7 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
     const int x = warp >> 2;                     // stream
     const int i = threadIdx.x & (TILE - 1);      // query row of its tile = TMEM lane
     const uint32_t lsel = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tSx = tS[x] + lsel, tOx = tO[x] + lsel;
+    const uint32_t tSx = tmem + x * M::S_STREAM + lsel, tOx = tmem + M::O + x * M::O_STREAM + lsel;
     const float c1 = p.scale * kLog2e;
     const float resc_raw = kRescale / p.scale;
     bool ok = true;
@@ -1074,7 +1089,7 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
           }
           tc_fence_after();
           if (active) {
-            const uint32_t tSh = tSx + hf * SUB;
+            const uint32_t tSh = tSx + hf * M::S_HALF;
             const int lim = hf ? nv.y : nv.x;
             float sv[SUB];
             tmem_ld32(tSh, sv);
@@ -1125,10 +1140,10 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
             const float nm = m == -INFINITY ? 0.f : -m * c1;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              uint32_t hi[16], lo[16];
-              exp32<NS>(sv + 32 * c, c1, nm, l2, hi, lo);
-              tmem_st16(tSh + 16 * c, hi);
-              if constexpr (NS == 2) tmem_st16(tSh + 32 + 16 * c, lo);
+              uint32_t w[NS][16];
+              exp32<NS>(sv + 32 * c, c1, nm, l2, w);
+#pragma unroll
+              for (int k = 0; k < NS; ++k) tmem_st16(tSh + 32 * k + 16 * c, w[k]);
             }
             tmem_wait_st();
           }
@@ -1378,11 +1393,11 @@ eta_status_t launch_attend_d(int gate, bool two, const CUtensorMap& mq, const CU
                              int P, cudaStream_t s) {
   switch (gate * 2 + (two ? 1 : 0)) {
     case 0: return launch_attend<D, NONE, 1>(mq, mq1, mk, mv, a, P, s);
-    case 1: return launch_attend<D, NONE, 2>(mq, mq1, mk, mv, a, P, s);
+    case 1: return launch_attend<D, NONE, 3>(mq, mq1, mk, mv, a, P, s);
     case 2: return launch_attend<D, HARD, 1>(mq, mq1, mk, mv, a, P, s);
-    case 3: return launch_attend<D, HARD, 2>(mq, mq1, mk, mv, a, P, s);
+    case 3: return launch_attend<D, HARD, 3>(mq, mq1, mk, mv, a, P, s);
     case 4: return launch_attend<D, SOFT, 1>(mq, mq1, mk, mv, a, P, s);
-    default: return launch_attend<D, SOFT, 2>(mq, mq1, mk, mv, a, P, s);
+    default: return launch_attend<D, SOFT, 3>(mq, mq1, mk, mv, a, P, s);
   }
 }
 

@@ -35,12 +35,16 @@ def _index_tensor(x, device) -> torch.Tensor:
     return torch.tensor(list(x), dtype=torch.int32, device=device)
 
 
-def _on(device, fn, *args, stream=None):
-    """Calls fn with `device` current and, unless one is given, its current stream."""
+def _on(device, stream, fn, *args):
+    """Calls fn with `device` and, if one is given, `stream` current: what fn makes of its
+    arguments (index tensors from lists, say) then belongs to the stream that reads it."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return fn(*args)
     if device.index == torch.cuda.current_device():
-        return fn(*args, stream=stream)
+        return fn(*args)
     with torch.cuda.device(device):
-        return fn(*args, stream=stream)
+        return fn(*args)
 
 
 class PagedKVCache:
@@ -88,11 +92,12 @@ class PagedKVCache:
         self.ws = torch.zeros(L.eta_page_workspace_size(self.dims, n_pages), dtype=torch.uint8,
                               device=self.device)
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._cu_one = torch.arange(B + 1, dtype=torch.int32, device=self.device)
         self.init()
 
     def init(self, stream=None):
         """Empties every row and frees every page."""
-        _on(self.device, L.eta_page_init, self.dims, self.n_pages, self.state, stream=stream)
+        _on(self.device, stream, L.eta_page_init, self.dims, self.n_pages, self.state)
 
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, cu_new=None, stream=None):
         """Writes new tokens behind every row's last one: k_new, v_new bf16
@@ -107,42 +112,51 @@ class PagedKVCache:
         if cu_new is None:
             if n_new != self.B:
                 raise ValueError("without cu_new there is one token for every row")
-            if not hasattr(self, "_cu_one"):
-                self._cu_one = torch.arange(self.B + 1, dtype=torch.int32, device=self.device)
             cu_new = self._cu_one
-        cu_new = _index_tensor(cu_new, self.device)
-        if cu_new.numel() != self.B + 1:
-            raise ValueError("cu_new has B + 1 entries")
-        _on(self.device, L.eta_page_append, self.dims, self.n_pages, self.state, self.K, self.V,
-            k_new, v_new, cu_new, n_new, self.ws, self.dev_status, stream=stream)
+
+        def call():
+            cu = _index_tensor(cu_new, self.device)
+            if cu.numel() != self.B + 1:
+                raise ValueError("cu_new has B + 1 entries")
+            L.eta_page_append(self.dims, self.n_pages, self.state, self.K, self.V, k_new, v_new,
+                              cu, n_new, self.ws, self.dev_status)
+        _on(self.device, stream, call)
+
+    def _pairs(self, src, dst):
+        src, dst = _index_tensor(src, self.device), _index_tensor(dst, self.device)
+        if src.numel() != dst.numel():
+            raise ValueError("src and dst differ in length")
+        return src, dst, src.numel()
 
     def fork(self, src, dst, stream=None):
         """Row dst[i] (empty) becomes a copy of row src[i]: whole pages are shared, the
         partly filled last one is copied."""
-        src, dst = _index_tensor(src, self.device), _index_tensor(dst, self.device)
-        if src.numel() != dst.numel():
-            raise ValueError("src and dst differ in length")
-        _on(self.device, L.eta_page_fork, self.dims, self.n_pages, self.state, self.K, self.V,
-            src, dst, src.numel(), self.ws, self.dev_status, stream=stream)
+        def call():
+            s, t, n = self._pairs(src, dst)
+            L.eta_page_fork(self.dims, self.n_pages, self.state, self.K, self.V, s, t, n, self.ws,
+                            self.dev_status)
+        _on(self.device, stream, call)
 
     def free(self, rows, stream=None):
         """Empties rows; pages that no row holds any more become free."""
-        rows = _index_tensor(rows, self.device)
-        _on(self.device, L.eta_page_free, self.dims, self.n_pages, self.state, rows,
-            rows.numel(), self.ws, self.dev_status, stream=stream)
+        def call():
+            r = _index_tensor(rows, self.device)
+            L.eta_page_free(self.dims, self.n_pages, self.state, r, r.numel(), self.ws,
+                            self.dev_status)
+        _on(self.device, stream, call)
 
     def compact(self, stream=None):
         """Moves the pages in use to the numbers below n_live = n_pages - n_free."""
-        _on(self.device, L.eta_page_compact, self.dims, self.n_pages, self.state, self.K, self.V,
-            self.ws, self.dev_status, stream=stream)
+        _on(self.device, stream, L.eta_page_compact, self.dims, self.n_pages, self.state, self.K,
+            self.V, self.ws, self.dev_status)
 
     def copy_pages(self, src, dst, stream=None):
         """Copies the contents of pages src[i] to pages dst[i]."""
-        src, dst = _index_tensor(src, self.device), _index_tensor(dst, self.device)
-        if src.numel() != dst.numel():
-            raise ValueError("src and dst differ in length")
-        _on(self.device, L.eta_page_copy, self.dims, self.n_pages, self.K, self.V, src, dst,
-            src.numel(), self.ws, self.dev_status, stream=stream)
+        def call():
+            s, t, n = self._pairs(src, dst)
+            L.eta_page_copy(self.dims, self.n_pages, self.K, self.V, s, t, n, self.ws,
+                            self.dev_status)
+        _on(self.device, stream, call)
 
     def check_status(self):
         """Synchronizes, reads the device status word, raises on any error bit."""
@@ -213,16 +227,18 @@ class PagedEtaDecoder:
     def build_meta(self, blk_begin: int = 0, blk_end: int = -1, stream=None):
         """Block metadata of blocks [blk_begin, blk_end) of every row (call it after a
         prefill, a fork or a free; append_update after a decode step's append)."""
-        if self.cent is None:
-            self._alloc_meta()
         c = self.cache
 
-        def call(stream=None):
+        def call():
+            if self.cent is None:
+                if torch.cuda.is_current_stream_capturing():
+                    raise ValueError("call build_meta once before it is captured")
+                self._alloc_meta()
             L.eta_paged_build_block_meta(self.dims, c.n_pages, c.K, c.V, c.table, c.lengths,
                                          blk_begin, blk_end, self.cent, self.rmax, self.var,
-                                         self.cnt, self.vsum, self.dev_status, stream,
-                                         self.vardim)
-        _on(self.device, call, stream=stream)
+                                         self.cnt, self.vsum, self.dev_status,
+                                         vardim=self.vardim)
+        _on(self.device, stream, call)
 
     def append_update(self, stream=None):
         """Recompute the tail block of every row (call after appending a token)."""
@@ -237,8 +253,8 @@ class PagedEtaDecoder:
             if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape
                                   or not t.is_contiguous() or t.device != self.device):
                 raise ValueError(f"{name} must be contiguous fp32 {shape} on {self.device}")
-        _on(self.device, L.eta_predict_tau, self.dims, q, W, bias, tau_const, self.tau,
-            self.dev_status, stream=stream)
+        _on(self.device, stream, L.eta_predict_tau, self.dims, q, W, bias, tau_const, self.tau,
+            self.dev_status)
         return self.tau
 
     def screen(self, q, tau=None, stream=None):
@@ -247,11 +263,11 @@ class PagedEtaDecoder:
             raise ValueError("screen needs build_meta first")
         tau = self.tau if tau is None else self._check_tau(tau)
 
-        def call(stream=None):
+        def call():
             L.eta_screen(self.dims, q, tau, self.cent, self.rmax, self.var, self.cnt, self.bound,
                          self.z, self.scale, self.head_mask, self.union_idx, self.union_cnt, None,
-                         self.head_cnt, self.ws_screen, self.dev_status, stream, self.vardim)
-        _on(self.device, call, stream=stream)
+                         self.head_cnt, self.ws_screen, self.dev_status, vardim=self.vardim)
+        _on(self.device, stream, call)
 
     # -- attention ----------------------------------------------------------------------
     def _check_q(self, q):
@@ -284,18 +300,18 @@ class PagedEtaDecoder:
             prune = "skip"
         else:
             idx, cnt, prune = self.union_idx, self.union_cnt, self.prune
-        _on(self.device, L.eta_paged_decode, self.dims, c.n_pages, q, tau, c.K, c.V, c.table,
+        _on(self.device, stream, L.eta_paged_decode, self.dims, c.n_pages, q, tau, c.K, c.V, c.table,
             c.lengths, idx, cnt, T, self.scale, prune, self.vsum, self.cnt, self.o, self.lse,
-            self.ws_decode, self.dev_status, stream=stream)
+            self.ws_decode, self.dev_status)
         return self.o, self.lse
 
     def dense_decode(self, q, stream=None):
         """Standard softmax attention over every key of every row (no gate)."""
         self._check_q(q)
         c = self.cache
-        _on(self.device, L.eta_paged_decode, self.dims, c.n_pages, q, None, c.K, c.V, c.table,
+        _on(self.device, stream, L.eta_paged_decode, self.dims, c.n_pages, q, None, c.K, c.V, c.table,
             c.lengths, None, None, 0.0, self.scale, "skip", None, None, self.o, self.lse,
-            self.ws_decode, self.dev_status, stream=stream)
+            self.ws_decode, self.dev_status)
         return self.o, self.lse
 
     def shared_decode(self, q, group_off, prefix_len, tau=None, stream=None):
@@ -305,22 +321,23 @@ class PagedEtaDecoder:
         [n_groups + 1], prefix_len int32 [n_groups] (lists are copied to the device)."""
         self._check_q(q)
         tau, T = self._gate(tau)
-        off, pre = _index_tensor(group_off, self.device), _index_tensor(prefix_len, self.device)
-        n = pre.numel()
-        if off.numel() != n + 1:
-            raise ValueError("group_off has one entry more than prefix_len")
-        if self.ws_shared is None or self.ws_shared[0] != n:
-            size = L.eta_shared_decode_workspace_size(self.dims, n)
-            if size == 0:
-                raise ValueError("between 1 and B groups")
-            if self.ws_shared is None or self.ws_shared[1].numel() < size:
-                self.ws_shared = (n, torch.empty(size, dtype=torch.uint8, device=self.device))
-            else:
-                self.ws_shared = (n, self.ws_shared[1])
         c = self.cache
-        _on(self.device, L.eta_shared_decode, self.dims, c.n_pages, n, q, tau, c.K, c.V, c.table,
-            c.lengths, off, pre, T, self.scale, self.o, self.lse, self.ws_shared[1],
-            self.dev_status, stream=stream)
+
+        def call():
+            off, pre = _index_tensor(group_off, self.device), _index_tensor(prefix_len, self.device)
+            n = pre.numel()
+            if not 1 <= n <= self.B:
+                raise ValueError("between 1 and B groups")
+            if off.numel() != n + 1:
+                raise ValueError("group_off has one entry more than prefix_len")
+            if self.ws_shared is None:
+                # for any number of groups: a captured call keeps its address
+                size = L.eta_shared_decode_workspace_size(self.dims, self.B)
+                self.ws_shared = torch.empty(size, dtype=torch.uint8, device=self.device)
+            L.eta_shared_decode(self.dims, c.n_pages, n, q, tau, c.K, c.V, c.table, c.lengths, off,
+                                pre, T, self.scale, self.o, self.lse, self.ws_shared,
+                                self.dev_status)
+        _on(self.device, stream, call)
         return self.o, self.lse
 
     def step(self, q, W=None, bias=None, tau_const=None, stream=None, append: bool = True):
