@@ -62,7 +62,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 enum Gate { NONE = 0, HARD = 1, SOFT = 2 };
 
 // ------------------------------------------------------------------------- work list
-// Costs in half microseconds, as measured (64 rows over 128K tokens, 4 KV heads): a key
+// Costs in about half microseconds, as measured (64 rows over 128K tokens, 4 KV heads): a key
 // tile of up to 256 or 128 queries, a key tile of a row's own, and what a row's own item
 // costs besides (its few tiles cannot fill the pipeline).  An item's tiles begin at 0 and
 // seg + t * cost; a CTA has the tiles that begin in its share of the costs.  With few
