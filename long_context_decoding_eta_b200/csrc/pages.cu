@@ -9,7 +9,9 @@
 // are one launch each: every CTA works the whole decision out for itself (a scan over the
 // rows or pairs, 1,024 at most), and what it was read from, the lengths and the free
 // count, is written by the CTA that finishes last.  Above 1,024 rows a plan kernel of one
-// CTA decides for all.
+// CTA decides for all.  Measured (us a launch, replayed): append of 64 rows, 11,000 tokens of
+// 2 KB, 9.9 (read + write 4.6 TB/s); free and fork of 6 rows 6.5 and 5.4, of 56 rows of 300 pages 11.5 and
+// 7.7; compaction of 2.06 GB 333 (6.2 TB/s), of 34 MB 13; 1,777 pages of 128 KB 84 (5.5 TB/s).
 #include <algorithm>
 
 #include "eta_common.cuh"

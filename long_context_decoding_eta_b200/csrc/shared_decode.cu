@@ -28,6 +28,12 @@
 //                        tiles of the one query tile, with accumulators of their own.
 //                        P overwrites S in tensor memory.
 //   shared_combine_kernel  joins the parts of every (row, head).
+//
+// 64 rows of 16 / 4 heads of 128 over a 128K-token prefix and up to 1,024 own tokens each,
+// bf16 output: 121 us a call with new inputs (105 as a replayed graph, part of the keys in
+// L2) for a floor of 52 (341 MB); the attend kernel alone runs at 45% of HBM, 47% of the
+// tensor pipe and 46% of the SFU, bound by the chain Q K^T - softmax - P V of its streams.
+// 4 rows of 2,048 + 64 tokens: 23 us, three launches' latency.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -920,7 +926,8 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t off = (uint64_t)(((kk >> 2) * HALF + (kk & 3) * 32) >> 4);
-          mma_ss(lead, tmem + x * M::S_STREAM + h * M::S_HALF, dqs + off, dks + off, idesc<SUB>(), kk > 0);
+          mma_ss(lead, tmem + x * M::S_STREAM + h * M::S_HALF, dqs + off, dks + off,
+                 idesc<SUB>(), kk > 0);
         }
         commit(lead, &ms->s_full[x][h]);
         if (h) {
@@ -943,7 +950,8 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
 #pragma unroll
           for (int kk = 0; kk < SUB / 16; ++kk)
             mma_ts(lead, tmem + M::O + x * M::O_STREAM,
-                   tmem + x * M::S_STREAM + h * M::S_HALF + term * 32 + kk * 8, dvs + (uint64_t)(kk * 2048 >> 4), id, (term > 0 || kk > 0) ? 1u : acc);
+                   tmem + x * M::S_STREAM + h * M::S_HALF + term * 32 + kk * 8,
+                   dvs + (uint64_t)(kk * 2048 >> 4), id, (term > 0 || kk > 0) ? 1u : acc);
         commit(lead, &ms->pv_done[x][h]);
         if (h) {
           commit(lead, &ms->kv_empty[vs]);
@@ -1024,7 +1032,8 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
     const int x = warp >> 2;                     // stream
     const int i = threadIdx.x & (TILE - 1);      // query row of its tile = TMEM lane
     const uint32_t lsel = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tSx = tmem + x * M::S_STREAM + lsel, tOx = tmem + M::O + x * M::O_STREAM + lsel;
+    const uint32_t tSx = tmem + x * M::S_STREAM + lsel;
+    const uint32_t tOx = tmem + M::O + x * M::O_STREAM + lsel;
     const float c1 = p.scale * kLog2e;
     const float resc_raw = kRescale / p.scale;
     bool ok = true;

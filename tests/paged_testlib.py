@@ -153,9 +153,9 @@ def attention(q, k, v, keep, tau, T, scale, p_eps, out_eps, gate_eps=2.0 ** -20)
     the scale and the base-2 argument of the exponential round twice more: with
     A = max scale * sum |q_i k_i|, |ds| <= (d + 4) 2^-24 A; a soft gate multiplies that by
     at most its slope, 1 + 0.28 |s| / T, and its sigmoid is off by gate_eps: 2^-20 from an
-    exponential and a division, 2^-10 from the approximate tanh.  A weight is then off by e_w = |ds'| + 2^-21 (approximate exponentials, two of
-    them through a rescaled maximum), its rounding adds p_eps, and sums of n terms in
-    tiles of 128 add (128 + n / 128) 2^-24.  Numerator and denominator err together:
+    exponential and a division, 2^-10 from the approximate tanh.  A weight is then off by
+    e_w = |ds'| + 2^-21 (approximate exponentials, two of them through a rescaled maximum),
+    its rounding adds p_eps, and sums of n terms in tiles of 128 add (128 + n / 128) 2^-24.  Numerator and denominator err together:
     |do| <= 2 (e_w + p_eps + e_sum) * sum p |v| / sum p, plus the output's own rounding;
     |dlse| <= e_w + e_sum + 2^-23 |lse|.
     """

@@ -132,6 +132,28 @@ def test_long_prefix_and_many_rows():
     run_and_check(c, 8, off, pre, None, torch.float32)
 
 
+def test_pages_past_32_bit_offsets():
+    """Two rows whose shared and own pages lie past 2^32 bytes of the pools."""
+    Hkv, d, blk, n_pages = 4, 128, 128, 40000          # 5.2 GB of keys
+    c = PagedKVCache(2, Hkv, d, blk, 20, n_pages)
+    ids = torch.arange(n_pages - 40, n_pages, dtype=torch.int32).flip(0).cuda()
+    gen = torch.Generator().manual_seed(5)
+    k, v = (torch.randn(40, Hkv, blk, d, generator=gen).to(torch.bfloat16).cuda() for _ in "kv")
+    c.K[ids.long()], c.V[ids.long()] = k, v
+    small = make_cache([20 * blk - 7] * 2, Hkv, d, blk)
+    order = small.table.view(-1).long()
+    small.K[order], small.V[order] = k, v
+    for x, first in ((c, ids), (small, small.table.view(-1).clone())):
+        x.table.copy_(first.view(2, 20))
+        x.table[1, :15] = x.table[0, :15]
+        x.lengths.fill_(20 * blk - 7)
+    q = torch.randn(2, 8, d, generator=gen).to(torch.bfloat16).cuda()
+    dec = PagedEtaDecoder(c, 8, T=None)
+    o, lse = dec.shared_decode(q, [0, 2], [15 * blk])
+    dec.check_status()
+    assert check(small, q, o, lse, None, None, p_eps=2.0 ** -24) == 16
+
+
 def test_the_same_bits_on_every_call():
     c, off, pre = shared_cache([(50, [50 * 64 + 7] * 9), (10, [700, 800])], 2, 128, 64, seed=3)
     dec, q, tau = run_and_check(c, 8, off, pre, 0.05, torch.float32)
