@@ -1089,6 +1089,7 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
                 *reinterpret_cast<uint4*>(vt + hh * HALF + c * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_async_smem();
+          __syncwarp();                          // the loads of S are the whole warp's
         }
 #pragma unroll 1
         for (int hf = 0; hf < 2; ++hf) {
@@ -1177,6 +1178,7 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             float ov[32];
+            __syncwarp();                        // together again behind the stores
             tmem_ld32(tOx + c * 32, ov);
             tmem_wait_ld32(ov);
             if (store && in) {
