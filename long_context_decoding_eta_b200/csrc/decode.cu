@@ -739,17 +739,34 @@ extern "C" eta_status_t eta_dense_decode(const eta_dims_t* dims, const eta_bf16_
 // The tensor-core decode with its blocks behind the page table (decode_paged_kernel): the
 // same shares, partial slots and combine as the contiguous decode, one table lookup per
 // block on the TMA warp, two positions ahead of its use.  Bound by HBM like it: 16% of the
-// blocks of 32 rows of 128K tokens (963 MB) in 180 us with the plan and the combine (5.4 TB/s),
-// 13 ragged rows of up to 20,011 tokens, all blocks, fp32 output (796 MB), in 129 us (6.2 TB/s).
+// blocks of 32 rows of 128K tokens (963 MB) in 179 us with the combine (5.4 TB/s),
+// 13 ragged rows of up to 20,011 tokens, all blocks, fp32 output (796 MB), in 127 us (6.3 TB/s).
 namespace eta {
+
+// Whether the decode lays out the shares itself, a launch fewer, instead of plan_kernel.  Each
+// CTA then goes over all pairs, which a launch before it does once: with 8 pairs 9.9 us
+// against 12.5, with 256 15.7 against 16.7, with 512 20.5 against 20.1, with 1024 29.1 against
+// 28.6 (d = 128, 100 to 200 tokens each).  Three terms of 8 heads need the plan's memory.
+constexpr int kPagedPlanInMaxRows = 256;
+static_assert(kPagedPlanInMaxRows <= tc::kFusedMaxRows, "the plan's shared memory");
+inline bool paged_plan_in(int R, int cols) { return R <= kPagedPlanInMaxRows && cols <= 16; }
 
 template <int G, bool GATE, int DD, int NS>
 eta_status_t launch_paged_t(const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mq,
                             const tc::TcParams& prm, int P, cudaStream_t s) {
+  if constexpr (NS * G <= 16) {
+    if (paged_plan_in(prm.R, NS * G)) {
+      constexpr int smem = tc::FUSED_SMEM_BYTES;
+      if (!set_smem_once<tc::decode_paged_kernel<G, GATE, DD, NS, true>>(smem))
+        return ETA_ERR_CUDA;
+      return launch_k(tc::decode_paged_kernel<G, GATE, DD, NS, true>, dim3(P), dim3(tc::NT), smem,
+                      s, mk, mv, mq, prm);
+    }
+  }
   constexpr int smem = NS * G <= 16 ? tc::SMEM_BYTES : tc::SMEM_BYTES_WIDE;
-  if (!set_smem_once<tc::decode_paged_kernel<G, GATE, DD, NS>>(smem)) return ETA_ERR_CUDA;
-  return launch_k(tc::decode_paged_kernel<G, GATE, DD, NS>, dim3(P), dim3(tc::NT), smem, s, mk,
-                  mv, mq, prm);
+  if (!set_smem_once<tc::decode_paged_kernel<G, GATE, DD, NS, false>>(smem)) return ETA_ERR_CUDA;
+  return launch_k(tc::decode_paged_kernel<G, GATE, DD, NS, false>, dim3(P), dim3(tc::NT), smem, s,
+                  mk, mv, mq, prm);
 }
 
 template <int G>
@@ -805,13 +822,18 @@ extern "C" eta_status_t eta_paged_decode(
       !make_map(&mv, V_pool, kv_rows, 64, dims->d) ||
       !make_map(&mq, q, (uint64_t)dims->B * dims->Hq, 16, dims->d))
     return ETA_ERR_CUDA;
-  st = union_idx ? launch_k(plan_kernel<false>, dim3(1), dim3(kPlanThreads), 0, s, R, dims->Hkv,
-                            NB, dims->blk, dims->T_max, union_cnt, lengths, P, row_off, cta_row,
-                            plan, dev_status)
-                 : launch_k(plan_kernel<true>, dim3(1), dim3(kPlanThreads), 0, s, R, dims->Hkv,
-                            NB, dims->blk, dims->T_max, union_cnt, lengths, P, row_off, cta_row,
-                            plan, dev_status);
-  if (st != ETA_OK) return st;
+  // an fp32 output takes P in three terms, so that the product with V is as exact as
+  // fp32 sums; a bf16 output's own rounding is far above the two-term split's 2^-16
+  const bool wide = o_format == ETA_OUT_F32, d64 = dims->d == 64, gate = tau != nullptr;
+  if (!paged_plan_in(R, (wide ? 3 : 2) * (dims->Hq / dims->Hkv))) {
+    st = union_idx ? launch_k(plan_kernel<false>, dim3(1), dim3(kPlanThreads), 0, s, R, dims->Hkv,
+                              NB, dims->blk, dims->T_max, union_cnt, lengths, P, row_off, cta_row,
+                              plan, dev_status)
+                   : launch_k(plan_kernel<true>, dim3(1), dim3(kPlanThreads), 0, s, R, dims->Hkv,
+                              NB, dims->blk, dims->T_max, union_cnt, lengths, P, row_off, cta_row,
+                              plan, dev_status);
+    if (st != ETA_OK) return st;
+  }
 
   tc::TcParams prm = {};
   prm.Hq = dims->Hq; prm.Hkv = dims->Hkv; prm.T_max = dims->T_max; prm.NB = NB;
@@ -820,9 +842,6 @@ extern "C" eta_status_t eta_paged_decode(
   prm.cta_row = cta_row; prm.plan = plan; prm.part_o = part_o; prm.part_ml = part_ml;
   prm.status = dev_status; prm.R = R; prm.counts = union_cnt; prm.row_off_g = row_off;
   prm.plan_g = plan; prm.table = table; prm.n_pages = n_pages;
-  // an fp32 output takes P in three terms, so that the product with V is as exact as
-  // fp32 sums; a bf16 output's own rounding is far above the two-term split's 2^-16
-  const bool wide = o_format == ETA_OUT_F32, d64 = dims->d == 64, gate = tau != nullptr;
   switch (dims->Hq / dims->Hkv) {
     case 1: st = launch_paged_g<1>(gate, d64, wide, mk, mv, mq, prm, P, s); break;
     case 2: st = launch_paged_g<2>(gate, d64, wide, mk, mv, mq, prm, P, s); break;

@@ -203,14 +203,15 @@ struct FuseCtx {
 // The fused step: every CTA lays out the CTA shares itself (prefix sum of per-row
 // admitted counts, exactly as plan_kernel) into its shared memory: row_off[0..R], fs->plan = {total,
 // share length}, fs->cta_row = the row holding position blockIdx * share.  Every
-// thread of the CTA calls it.
-ETA_DEV void plan_local(const int32_t* counts, int R, int NB, int* row_off, FuseSmem* fs,
-                        int32_t* status) {
+// thread of the CTA calls it.  count(r): the admitted blocks of pair r.
+template <typename Count>
+ETA_DEV void plan_local_of(Count count, int R, int NB, int* row_off, FuseSmem* fs,
+                           int32_t* status) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int carry = 0;
   for (int base = 0; base < R; base += NT) {
     const int r = base + threadIdx.x;
-    int c = r < R ? __ldcg(counts + r) : 0;
+    int c = r < R ? count(r) : 0;
     if (c < 0 || c > NB) {
       set_status(status, ETA_DEVSTAT_BAD_BLOCK);
       c = min(max(c, 0), NB);
@@ -251,6 +252,11 @@ ETA_DEV void plan_local(const int32_t* counts, int R, int NB, int* row_off, Fuse
   __syncthreads();
 }
 
+ETA_DEV void plan_local(const int32_t* counts, int R, int NB, int* row_off, FuseSmem* fs,
+                        int32_t* status) {
+  plan_local_of([&](int r) { return __ldcg(counts + r); }, R, NB, row_off, fs, status);
+}
+
 // The decode of one CTA share.  `smem` is the CTA's dynamic shared memory aligned
 // to 1024 bytes.  Every thread of the CTA calls it.
 // LOCAL (the fused step): the plan, the prefix sums and the CTA's first row are the
@@ -266,9 +272,9 @@ ETA_DEV void plan_local(const int32_t* counts, int R, int NB, int* row_off, Fuse
 // those lines earlier in the launch (the screening reads tau with L2-only loads).
 // PDL_IN (the standalone kernel): the shared-memory and TMEM setup runs before the
 // wait for the previous grid, so it overlaps that grid's tail; the plan is read after.
-// PLAN_IN (with PDL_IN, sparse): no plan launch; every CTA lays the shares out itself
-// (plan_local, from the admitted counts) and CTA 0 publishes row_off and the plan
-// for the combine launch.
+// PLAN_IN (with PDL_IN, sparse or paged): no plan launch; every CTA lays the shares out
+// itself (plan_local, from the admitted counts; from the lengths for all blocks of a paged
+// cache) and CTA 0 publishes row_off and the plan for the combine launch.
 // DD (head dimension) 128, or 64: then one 64-dim box per K/V sub-tile and for the
 // query rows, QK^T in 4 steps of 16 dims, and P V still M = 128 (the V tile's upper
 // 64-dim half stays zero, so those accumulator rows are zero and not written out).
@@ -286,9 +292,10 @@ ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const C
   static_assert(!(LOCAL && DENSE), "the in-kernel merge is for the sparse decode");
   static_assert(!FLAGS || LOCAL, "flags come with the local plan");
   static_assert(!PLAN_IN || (PDL_IN && (!DENSE || PAGED) && !LOCAL),
-                "plan in the standalone sparse decode");
-  static_assert(NS == 2 || (NS == 3 && PAGED && !PLAN_IN), "three terms in the paged decode");
+                "plan in the standalone sparse or paged decode");
   constexpr int NP = NS * G <= 16 ? 16 : 32;          // columns of P^T and of O^T
+  static_assert(NS == 2 || (NS == 3 && PAGED && !(PLAN_IN && NP == 32)),
+                "three terms in the paged decode; the plan's memory or a wide P^T's");
   constexpr int OFF_P1 = NP == 16 ? SM_P + PBUF : SM_PWIDE;   // the second P^T buffer
   constexpr int TCOLS = NP == 16 ? kTmemCols : kTmemColsWide;
   constexpr uint32_t kIdescPVn =
@@ -352,7 +359,21 @@ ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const C
     if constexpr (PLAN_IN) {
       FuseSmem* fs = reinterpret_cast<FuseSmem*>(smem + SM_FUSE);
       int* ro = reinterpret_cast<int*>(smem + SM_ROWOFF);
-      plan_local(p.counts, p.R, p.NB, ro, fs, p.status);
+      if constexpr (PAGED) {
+        plan_local_of(
+            [&](int r) -> int {
+              if (p.union_idx) return __ldcg(p.counts + r);
+              int len = __ldcg(p.lengths + r / p.Hkv);
+              if (len < 0 || len > p.T_max) {
+                set_status(p.status, ETA_DEVSTAT_BAD_LENGTH);
+                len = min(max(len, 0), p.T_max);
+              }
+              return (len + p.blk - 1) / p.blk;
+            },
+            p.R, p.NB, ro, fs, p.status);
+      } else {
+        plan_local(p.counts, p.R, p.NB, ro, fs, p.status);
+      }
       if (blockIdx.x == 0) {
         for (int r = threadIdx.x; r <= p.R; r += NT) p.row_off_g[r] = ro[r];
         if (threadIdx.x == 0) {
@@ -811,16 +832,16 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                                                              FuseCtx{});
 }
 
-// The decode of a paged cache (GATE: thresholds given).  NS: see decode_tc_body.
-template <int G, bool GATE, int DD, int NS>
+// The decode of a paged cache (GATE: thresholds given).  NS, PLAN_IN: see decode_tc_body.
+template <int G, bool GATE, int DD, int NS, bool PLAN_IN>
 __global__ void __launch_bounds__(NT, 1)
 decode_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const __grid_constant__ CUtensorMap tmQ, const TcParams p) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  decode_tc_body<G, !GATE, false, false, true, false, DD, true, NS>(smem, &tmK, &tmV, &tmQ, p,
-                                                                    FuseCtx{});
+  decode_tc_body<G, !GATE, false, false, true, PLAN_IN, DD, true, NS>(smem, &tmK, &tmV, &tmQ, p,
+                                                                      FuseCtx{});
 }
 
 }  // namespace tc

@@ -251,3 +251,49 @@ def test_layer_refuses_wrong_tensors():
                  torch.zeros(3, 2, 64, device="cuda").bfloat16())
     with pytest.raises(ValueError):
         c.fork([0], [1, 1])
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B", [32, 33, 257])
+def test_many_rows_on_both_sides_of_the_plan_launch(B, out):
+    """256 (row, KV head) pairs are laid out by the decode itself, more by a launch before it."""
+    lens = [random.Random(B * 1000 + b).choice([0, 1, 63, 64, 65, 130, 200]) for b in range(B)]
+    c = make_cache(lens, 8, 64, 64, seed=B, poison=True)
+    gen = torch.Generator().manual_seed(B)
+    q = torch.randn(B, 8, 64, generator=gen).to(torch.bfloat16).cuda()
+    dec = PagedEtaDecoder(c, 8, T=None, out_dtype=out)
+    o, lse = dec.decode(q, all_blocks=True)
+    dec.check_status()
+    assert check(c, q, o, lse, None, None, p_eps=P_EPS[out]) == 8 * sum(n > 0 for n in lens)
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (8, 1)])
+def test_a_cache_with_nothing_in_it(Hq, Hkv, out):
+    c = make_cache([0, 0, 0], Hkv, 128, 64, max_pages=4)
+    q = torch.ones(3, Hq, 128, dtype=torch.bfloat16, device="cuda")
+    dec = PagedEtaDecoder(c, Hq, T=None, out_dtype=out)
+    for _ in range(2):
+        o, lse = dec.decode(q, all_blocks=True)
+        dec.check_status()
+        assert torch.all(o == 0) and torch.all(lse == -math.inf)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(4, 2), (8, 1)])
+def test_a_bad_length_is_reported_and_clamped(Hq, Hkv):
+    """A length below zero reads as 0, one past the table as the table's end."""
+    c = make_cache([64, 256, 130], Hkv, 64, 64, max_pages=4)
+    q = torch.randn(3, Hq, 64, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    q = q.cuda()
+    dec = PagedEtaDecoder(c, Hq, T=None)
+    o, lse = (t.clone() for t in dec.decode(q, all_blocks=True))
+    dec.check_status()
+    c.lengths[0] = -3
+    c.lengths[1] = 1000
+    o2, lse2 = dec.decode(q, all_blocks=True)
+    with pytest.raises(L.EtaError):
+        dec.check_status()
+    assert torch.all(o2[0] == 0) and torch.all(lse2[0] == -math.inf)
+    # the same weights split among the CTAs in another way: two fp32 sums of 256 terms whose
+    # weights add up to one
+    assert torch.all((o2[1:] - o[1:]).abs() <= 2 * 256 * 2.0 ** -24 * c.V.abs().max().float())
