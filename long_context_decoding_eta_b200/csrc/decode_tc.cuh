@@ -315,9 +315,8 @@ ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const C
     e = min(a + chunk, Ntot);
   }
 
-  // zero the V halves and the P buffers once: every row the PV MMA reads is then
-  // finite (TMA only overwrites them with cache rows, and rows past a sequence's
-  // length are zeroed again by the softmax warps before use)
+  // zero the V halves and the P buffers once (d = 64 leaves the upper halves so); the
+  // rows of V without a key are zeroed by the softmax warps before each use
   for (int s = 0; s < NSTAGE; ++s) {
     uint4* v = reinterpret_cast<uint4*>(smem + s * STAGE_BYTES + OFF_V0);
     for (int i = threadIdx.x; i < 2 * HALF / 16; i += NT) v[i] = make_uint4(0, 0, 0, 0);
@@ -755,8 +754,10 @@ ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const C
         const float wm = warp_max(sp[h]);
         if (lane == 0) ms->red[sb][warp][h] = wm;
       }
-      // a partial sub-tile: zero the V rows past the sequence end (finite inputs to PV)
-      if (!valid && nv > 0) {
+      // zero the V rows without a key: past the sequence end in a partial sub-tile, and all
+      // 64 of one that was not loaded, where another row's values, finite or not, would
+      // meet the zero weights (0 * inf)
+      if (!valid) {
         unsigned char* st = smem + s * STAGE_BYTES;
         uint4* r0 = reinterpret_cast<uint4*>(st + OFF_V0 + t * 128);
         uint4* r1 = reinterpret_cast<uint4*>(st + OFF_V1 + t * 128);
