@@ -756,13 +756,17 @@ ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const C
       }
       // zero the V rows without a key: past the sequence end in a partial sub-tile, and all
       // 64 of one that was not loaded, where another row's values, finite or not, would
-      // meet the zero weights (0 * inf)
+      // meet the zero weights (0 * inf).  The lanes start at different 16-byte columns, so
+      // that a warp's stores spread over the banks
       if (!valid) {
         unsigned char* st = smem + s * STAGE_BYTES;
         uint4* r0 = reinterpret_cast<uint4*>(st + OFF_V0 + t * 128);
         uint4* r1 = reinterpret_cast<uint4*>(st + OFF_V1 + t * 128);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) { r0[c] = make_uint4(0, 0, 0, 0); r1[c] = make_uint4(0, 0, 0, 0); }
+        for (int c = 0; c < 8; ++c) {
+          r0[(c + t) & 7] = make_uint4(0, 0, 0, 0);
+          r1[(c + t) & 7] = make_uint4(0, 0, 0, 0);
+        }
       }
       named_bar_sync(1, NWARP_SM * 32);
       float alpha[G];
