@@ -600,7 +600,8 @@ ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const C
       m_run[h] = -INFINITY; l_part[h] = 0.f; o_acc[h] = 0.f; alpha_prev[h] = 0.f;
     }
     float tau_h[G];
-    int cur = -1;
+    // the pair of the last stage, and the first pair of the share without a partial result
+    int cur = -1, todo = (LOCAL || PLAN_IN) ? cta_row[0] : cta_row[blockIdx.x];
     bool pending = false;   // stage i-1 still has to be folded into o_acc
     bool ok = true;
 
@@ -710,6 +711,13 @@ ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const C
       }
     };
 
+    // Partial results of the pairs before `row`: that of `cur`, and empty ones (m = -inf,
+    // l = 0) of pairs whose blocks were all skipped, since the merge counts on them.
+    auto flush_before = [&](int row) {
+      for (; todo < row; ++todo)
+        if (todo == cur || row_off[todo + 1] > row_off[todo]) flush(todo);
+    };
+
     int i = 0;
     for (;; ++i) {
       const int s = i % NSTAGE;
@@ -721,7 +729,7 @@ ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const C
           if (!correct(i - 1)) { ok = false; break; }
           pending = false;
         }
-        if (cur >= 0) flush(cur);
+        flush_before(inf.row);
         cur = inf.row;
         if constexpr (!DENSE) {
           const int b = cur / p.Hkv, g = cur % p.Hkv;
@@ -813,7 +821,11 @@ ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const C
     }
     // the last stage: its PV is issued after the end marker
     if (ok && pending) ok = correct(i - 1);
-    if (ok && cur >= 0) flush(cur);
+    if (ok) {
+      int end = max(cur + 1, todo);             // behind the share's last pair
+      while (end < p.R && row_off[end] < e) ++end;
+      flush_before(end);
+    }
     if (!ok) {
       if (t == 0) set_status(p.status, ETA_DEVSTAT_TIMEOUT);
       *abort_flag = 1;

@@ -50,3 +50,84 @@ def test_values_of_other_rows_stay_out(form):
     got = run()
     assert torch.equal(got[::2], want[::2])
     assert not torch.isfinite(got[1::2]).any()
+
+
+def take_status(dec):
+    torch.cuda.synchronize()
+    s = int(dec.dev_status)
+    dec.dev_status.zero_()
+    return s
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B", [3, 130])
+def test_a_share_without_a_key_is_an_empty_part(B, out):
+    """Row 0 keeps its first and last block, row 1 nothing: with at most 4 blocks a share
+    some shares hold skipped blocks alone.  6 and 260 (row, KV head) pairs: the shares laid
+    out by the decode and by a launch before it."""
+    lens = [640, 40, 300] + [70] * (B - 3)
+    c = make_cache(lens, 2, 64, 64, seed=7)
+    q = torch.randn(B, 4, 64, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    dec = PagedEtaDecoder(c, 4, T=None, out_dtype=out)
+    dec.dense_decode(q)
+    dec.check_status()
+    c.table[0, 1:9] = torch.tensor([-1, c.n_pages] * 4, dtype=torch.int32)
+    c.table[1, 0] = c.n_pages + 1
+    dec.ws_decode.fill_(0x3F)                # a part that is not written weighs in
+    o, lse = dec.dense_decode(q)
+    assert take_status(dec) == L.DEVSTAT_BAD_BLOCK
+    c.table[0, 1:9] = c.table[1, 0] = 0      # for the oracle's gather: left out below
+    blocks = [[[0, 9]] * 2, [[]] * 2, [list(range(5))] * 2] + [[[0, 1]] * 2] * (B - 3)
+    assert check(c, q, o, lse, None, None, blocks, p_eps=P_EPS[out]) == 4 * (B - 1)
+
+
+def test_block_lists_of_a_row_that_was_freed():
+    """The lists of the step before: the freed row reads as empty, the others as they are."""
+    c = make_cache([640, 500, 300], 2, 64, 64, seed=11)
+    dec = PagedEtaDecoder(c, 4, T=None)
+    for b, n in enumerate((10, 8, 5)):
+        dec.union_idx[b, :, :n] = torch.arange(n, dtype=torch.int32, device="cuda")
+        dec.union_cnt[b] = n
+    q = torch.randn(3, 4, 64, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16).cuda()
+    dec.decode(q)
+    dec.check_status()
+    c.free([1])
+    dec.ws_decode.fill_(0x3F)
+    o, lse = dec.decode(q)
+    assert take_status(dec) == L.DEVSTAT_BAD_BLOCK
+    blocks = [[list(range(n))] * 2 for n in (10, 0, 5)]
+    assert check(c, q, o, lse, None, None, blocks, p_eps=2.0 ** -24) == 8
+
+
+@pytest.mark.parametrize("B", [3, 42])
+@pytest.mark.parametrize("engine", ["tcgen05"])
+def test_contiguous_lists_past_a_rows_end(engine, B):
+    """The contiguous decode on a list that reaches past a shortened row, and past an empty
+    one: the same as with the lists cut at the rows' ends."""
+    w = synth.MID.with_(B=B, ctx=1024, seed=51)
+    g = {k: (v.cuda() if isinstance(v, torch.Tensor) else v)
+         for k, v in synth.generate(w, "cpu").items()}
+    dec = EtaDecoder(g["K"], g["V"], g["lengths"], w.Hq, w.blk, T=0.0)
+    NB = dec.NB
+    dec.tau.fill_(-math.inf)
+    dec.union_idx[:] = torch.arange(NB, dtype=torch.int32, device="cuda")
+    dec.union_cnt.fill_(NB)
+    dec.lengths.copy_(torch.tensor([1024, 0, 256] * (B // 3), dtype=torch.int32))
+    L.eta_set_decode_engine(engine)
+    try:
+        dec.ws_decode.fill_(0x3F)
+        dec.decode(g["q"])
+        assert take_status(dec) == L.DEVSTAT_BAD_BLOCK
+        o, lse = dec.o.clone(), dec.lse.clone()
+        dec.union_cnt.copy_(torch.tensor([[NB], [0], [256 // w.blk]] * (B // 3)).expand(B, w.Hkv))
+        dec.decode(g["q"])
+        dec.check_status()
+    finally:
+        L.eta_set_decode_engine("auto")
+    assert torch.all(o[1::3] == 0) and torch.all(lse[1::3] == -math.inf)
+    # cut into other shares: half steps of up to 16 merged parts in numerator and
+    # denominator, weights that add up to one, |v| below 7
+    assert torch.all((o - dec.o).abs() <= 2 * 16 * 2.0 ** -24 * 7)
+    keep = torch.isfinite(lse)
+    assert torch.all((lse - dec.lse).abs()[keep] <= 2 * 16 * 2.0 ** -24 * 8)
+    assert torch.equal(keep, torch.isfinite(dec.lse))
