@@ -213,8 +213,18 @@ __global__ void __launch_bounds__((NCW + 1) * 32, 1) decode_kernel(const DecodeP
   float* pw = reinterpret_cast<float*>(smem + C::OFF_PW) + warp * 32;
   const int hl = lane % G;  // head of this lane's softmax slot
   float qr[G][DPL], o[G][DPL];
-  float m_run = -INFINITY, l_run = 0.f, tau_l = 0.f;
+  float m_run, l_run, tau_l = 0.f;
   int cur = -1;
+
+  auto reset = [&] {
+#pragma unroll
+    for (int h = 0; h < G; ++h)
+#pragma unroll
+      for (int i = 0; i < DPL; ++i) o[h][i] = 0.f;
+    m_run = -INFINITY;
+    l_run = 0.f;
+  };
+  reset();
 
   auto flush = [&](int row) {
 #pragma unroll
@@ -249,6 +259,7 @@ __global__ void __launch_bounds__((NCW + 1) * 32, 1) decode_kernel(const DecodeP
       }
     }
     named_bar_sync(1, NCW * 32);
+    reset();
   };
 
   auto start_row = [&](int row) {
@@ -259,17 +270,14 @@ __global__ void __launch_bounds__((NCW + 1) * 32, 1) decode_kernel(const DecodeP
     for (int h = 0; h < G; ++h) {
       lds_row<DPL>(p.q + (qh0 + h) * D + lane * DPL, qr[h]);
 #pragma unroll
-      for (int i = 0; i < DPL; ++i) {
-        bad |= !isfinite(qr[h][i]);
-        o[h][i] = 0.f;
-      }
+      for (int i = 0; i < DPL; ++i) bad |= !isfinite(qr[h][i]);
     }
     if (bad) set_status(p.status, ETA_DEVSTAT_NONFINITE_Q);
     if constexpr (!DENSE) tau_l = p.tau[qh0 + hl];
-    m_run = -INFINITY;
-    l_run = 0.f;
   };
 
+  // the first pair of the share without a partial result
+  int todo = p.cta_row[blockIdx.x];
   int it = 0;
   while (true) {
     const int s = it % NSTAGES;
@@ -280,10 +288,18 @@ __global__ void __launch_bounds__((NCW + 1) * 32, 1) decode_kernel(const DecodeP
       return;
     }
     const StageInfo inf = info[s];
-    if (inf.flags & kStageEnd) break;
-    if (inf.row != cur) {
-      if (cur >= 0) flush(cur);
-      cur = inf.row;
+    int row = inf.row;
+    if (inf.flags & kStageEnd) {
+      row = max(cur + 1, todo);          // behind the share's last pair
+      while (row < p.R && p.row_off[row] < e) ++row;
+    }
+    if (row != cur) {
+      // the partial result of `cur`, and empty ones (m = -inf, l = 0) of the pairs before
+      // `row` whose blocks were all skipped, since the merge counts on them
+      for (; todo < row; ++todo)
+        if (todo == cur || p.row_off[todo + 1] > p.row_off[todo]) flush(todo);
+      if (inf.flags & kStageEnd) break;
+      cur = row;
       start_row(cur);
     }
     const eta_bf16_t* sK = reinterpret_cast<const eta_bf16_t*>(smem + C::OFF_K + s * C::TILE);
@@ -357,7 +373,6 @@ __global__ void __launch_bounds__((NCW + 1) * 32, 1) decode_kernel(const DecodeP
     if (lane == 0) mbar_arrive(&empty[s]);
     ++it;
   }
-  if (cur >= 0) flush(cur);
 }
 
 // Prefix sum of admitted blocks per (row, KV head) pair and the CTA shares.

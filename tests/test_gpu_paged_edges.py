@@ -100,7 +100,7 @@ def test_block_lists_of_a_row_that_was_freed():
 
 
 @pytest.mark.parametrize("B", [3, 42])
-@pytest.mark.parametrize("engine", ["tcgen05"])
+@pytest.mark.parametrize("engine", ["tcgen05", "fma"])
 def test_contiguous_lists_past_a_rows_end(engine, B):
     """The contiguous decode on a list that reaches past a shortened row, and past an empty
     one: the same as with the lists cut at the rows' ends."""
