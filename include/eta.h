@@ -234,6 +234,7 @@ eta_status_t eta_screen(const eta_dims_t* dims, const eta_bf16_t* q, const float
  *   o[b,h] = sum_t e^{s'_t} v_t / sum_t e^{s'_t},   lse[b,h] = log sum_t e^{s'_t}
  * ETA_PRUNE_SKIP: pruned blocks are absent from the softmax; an empty union gives
  *   o = 0, lse = -inf.
+ * A NaN among a head's gated scores, or one of +inf, makes its o and lse NaN.
  * ETA_PRUNE_FLOOR: every valid key of a pruned block enters with logit 0 (its
  *   hard-gated value), using cnt and vsum from eta_build_block_meta (both required).
  * Split-KV over the admitted list (every CTA streams an equal share of admitted
@@ -334,7 +335,8 @@ eta_status_t eta_decode_step(const eta_dims_t* dims, const eta_bf16_t* q, const 
  * the decode of the whole cache: screening is per block, so each shard admits exactly
  * the blocks of the whole cache's union that lie in its range.
  *   M = max_p lse_p;  L = sum_p e^(lse_p - M);  o = sum_p e^(lse_p - M) o_p / L;
- *   lse = M + log L;  parts with lse_p = -inf add nothing; all empty: o = 0, lse = -inf.
+ *   lse = M + log L;  parts with lse_p = -inf add nothing; all empty: o = 0, lse = -inf;
+ *   a NaN lse_p makes the row NaN.
  * o_parts fp32 [n_parts, n_rows, d], lse_parts fp32 [n_parts, n_rows] (device);
  * o fp32 [n_rows, d], lse fp32 [n_rows] (device, may not alias the parts).
  * n_rows = B * Hq; d in {64, 128}; n_parts >= 1 (else ETA_ERR_INVALID_ARG).
@@ -607,7 +609,7 @@ eta_status_t eta_paged_decode(const eta_dims_t* dims, int32_t n_pages, const eta
  * and is read by itself, as is every row of a group of one.  The page numbers of the
  * prefix come from the group's first row that is long enough: a row of the group whose
  * table holds other pages there gets the group's keys, not its own.  Rows of length 0
- * give o = 0, lse = -inf.
+ * give o = 0, lse = -inf; NaN and +inf scores as eta_decode.
  * The prefix of up to 256 (row, head) pairs of one KV head is one pass of tensor-core
  * tiles (S = Q K^T, O += P V, 128 keys each) over its keys; a row's own keys are a pass
  * of their own; all passes are cut into shares of equal cost, one per SM.  bf16 output:

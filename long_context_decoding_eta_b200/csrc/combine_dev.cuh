@@ -133,13 +133,13 @@ ETA_DEV void combine_merge(const float* part_ml, const float* part_o, int r, int
 }
 
 // o[oh] = O / L and lse[oh] = M + log L; an empty softmax (L = 0) gives o = 0,
-// lse = -inf.
+// lse = -inf, and L = NaN (a NaN score, or one of +inf) passes on as NaN.
 ETA_DEV void store_out(float* p, float v) { *p = v; }
 ETA_DEV void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
 template <int D, typename OutT>
 ETA_DEV void combine_store(OutT* o, float* lse, size_t oh, int dd, float M, float L, float Oh) {
-  if (L > 0.f) {
+  if (L != 0.f) {
     store_out(o + oh * D + dd, Oh / L);
     if (dd == 0) lse[oh] = M + logf(L);
   } else {

@@ -244,13 +244,12 @@ __global__ void __launch_bounds__((NCW + 1) * 32, 1) decode_kernel(const DecodeP
 #pragma unroll
       for (int w = 0; w < NCW; ++w) M = fmaxf(M, mml[(w * G + h) * 2]);
       float O = 0.f, L = 0.f;
-      if (M != -INFINITY) {
 #pragma unroll
-        for (int w = 0; w < NCW; ++w) {
-          const float sc = __expf(mml[(w * G + h) * 2] - M);
-          O = fmaf(mo[(w * G + h) * D + dd], sc, O);
-          L = fmaf(mml[(w * G + h) * 2 + 1], sc, L);
-        }
+      for (int w = 0; w < NCW; ++w) {
+        const float m = mml[(w * G + h) * 2];
+        const float sc = m == -INFINITY ? 0.f : __expf(m - M);   // a NaN sum passes on
+        O = fmaf(mo[(w * G + h) * D + dd], sc, O);
+        L = fmaf(mml[(w * G + h) * 2 + 1], sc, L);
       }
       p.part_o[(slot * G + h) * D + dd] = O;
       if (dd == 0) {

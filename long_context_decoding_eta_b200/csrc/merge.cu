@@ -25,14 +25,13 @@ __global__ void __launch_bounds__(128) lse_merge_kernel(int n_parts, int n_rows,
   float M = -INFINITY;
   for (int p = 0; p < n_parts; ++p) M = fmaxf(M, lse_parts[(size_t)p * n_rows + row]);
   float L = 0.f, O = 0.f;
-  if (M != -INFINITY) {
-    for (int p = 0; p < n_parts; ++p) {
-      const float w = expf(lse_parts[(size_t)p * n_rows + row] - M);   // 0 for an empty part
-      L += w;
-      O = fmaf(w, o_parts[((size_t)p * n_rows + row) * d + dd], O);
-    }
+  for (int p = 0; p < n_parts; ++p) {
+    const float x = lse_parts[(size_t)p * n_rows + row];
+    const float w = x == -INFINITY ? 0.f : expf(x - M);   // 0 for an empty part; NaN passes on
+    L += w;
+    O = fmaf(w, o_parts[((size_t)p * n_rows + row) * d + dd], O);
   }
-  if (L > 0.f) {
+  if (L != 0.f) {
     o[(size_t)row * d + dd] = O / L;
     if (dd == 0) lse[row] = M + logf(L);
   } else {

@@ -1311,7 +1311,7 @@ shared_combine_kernel(const AttendParams p, OutT* __restrict__ o, float* __restr
   l = over_threads(l, [](float a, float c) { return a + c; });
   const size_t head0 = (size_t)b * p.Hq + kvh * G;
   if (tid < G) {
-    lse[head0 + tid] = l > 0.f ? mx + logf(l) : -INFINITY;
+    lse[head0 + tid] = l != 0.f ? mx + logf(l) : -INFINITY;   // NaN passes on
     red[0][tid] = l;
   }
   // head fastest: the G heads of 4 dims are side by side in a slot
@@ -1342,7 +1342,7 @@ shared_combine_kernel(const AttendParams p, OutT* __restrict__ o, float* __restr
       a.w += y.w;
     }
     const float L = red[0][h];
-    if (L > 0.f) {
+    if (L != 0.f) {
       a.x /= L;
       a.y /= L;
       a.z /= L;

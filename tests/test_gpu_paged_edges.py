@@ -131,3 +131,87 @@ def test_contiguous_lists_past_a_rows_end(engine, B):
     keep = torch.isfinite(lse)
     assert torch.all((lse - dec.lse).abs()[keep] <= 2 * 16 * 2.0 ** -24 * 8)
     assert torch.equal(keep, torch.isfinite(dec.lse))
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T", [None, 0.05])
+@pytest.mark.parametrize("form", ["paged", "shared"])
+def test_nan_is_not_an_empty_row(form, T, out):
+    """A NaN key or query, or a score of +inf (inf - inf in its softmax), gives NaN outputs
+    in the heads that attend to it; the others and empty rows are as without it."""
+    Hq, Hkv, d = 4, 2, 64
+    lens = [300, 260, 0, 500, 130]
+    c = make_cache(lens, Hkv, d, 64, seed=21)
+    c.table[1, :3] = c.table[0, :3]
+    q = torch.randn(5, Hq, d, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    q[4, 2, 0] = 1.0
+    tau = torch.full((5, Hq), 0.3, device="cuda")
+    dec = PagedEtaDecoder(c, Hq, T=T, out_dtype=out)
+
+    def run():
+        if form == "paged":
+            o, lse = dec.decode(q, tau=tau, all_blocks=True)
+        else:
+            o, lse = dec.shared_decode(q, [0, 2, 5], [3 * 64, 0], tau=tau)
+        dec.check_status()
+        return o.clone(), lse.clone()
+
+    o0, l0 = run()
+    bad = torch.zeros(5, Hq, dtype=torch.bool, device="cuda")
+    c.K[c.table[0, 3].long(), 0, 5] = math.nan      # a key of row 0's own, KV head 0
+    bad[0, :2] = True
+    q[3, 1, 7] = math.nan                           # a query
+    bad[3, 1] = True
+    c.K[c.table[4, 2].long(), 1, 1] = 0.0           # row 4, KV head 1: s = +inf in head 2,
+    c.K[c.table[4, 2].long(), 1, 1, 0] = math.inf   # whose q[0] is 1; head 3's is set below
+    q[4, 3, 0] = -1.0                               # s = -inf: weight 0
+    bad[4, 2] = True
+    bad[4, 3] = T is not None                       # -inf times the gate's 0
+    o, lse = run()
+    assert torch.equal(torch.isnan(o).all(-1), bad) and torch.equal(torch.isnan(o).any(-1), bad)
+    assert torch.equal(torch.isnan(lse), bad)
+    same = ~bad
+    same[4, 3] = False                              # its query changed
+    assert torch.equal(o[same], o0[same]) and torch.equal(lse[same], l0[same])
+    assert torch.all(o[2] == 0) and torch.all(lse[2] == -math.inf)
+
+
+@pytest.mark.parametrize("engine", ["tcgen05", "fma"])
+def test_nan_in_the_contiguous_engines(engine):
+    """As above behind contiguous rows; row 1's scores are all NaN."""
+    w = synth.MID.with_(B=3, ctx=1024, seed=52)
+    g = {k: (v.cuda() if isinstance(v, torch.Tensor) else v)
+         for k, v in synth.generate(w, "cpu").items()}
+    g["lengths"][2] = 0
+    dec = EtaDecoder(g["K"], g["V"], g["lengths"], w.Hq, w.blk, T=0.0)
+    L.eta_set_decode_engine(engine)
+    try:
+        dec.dense_decode(g["q"])
+        dec.check_status()
+        o, lse = dec.o.clone(), dec.lse.clone()
+        g["K"][0, 1, 700] = math.nan
+        g["K"][1, 3] = math.nan
+        dec.dense_decode(g["q"])
+        dec.check_status()
+    finally:
+        L.eta_set_decode_engine("auto")
+    bad = torch.zeros(3, w.Hq, dtype=torch.bool, device="cuda")
+    bad[0, w.G:2 * w.G] = bad[1, 3 * w.G:] = True
+    assert torch.equal(torch.isnan(dec.lse), bad) and torch.equal(torch.isnan(dec.o).all(-1), bad)
+    assert torch.equal(dec.o[~bad], o[~bad]) and torch.equal(dec.lse[~bad], lse[~bad])
+    assert torch.all(o[2] == 0) and torch.all(lse[2] == -math.inf)
+
+
+def test_merge_keeps_nan():
+    """A part that is NaN makes the merged row NaN; parts without a key do not count."""
+    o = torch.randn(3, 4, 64, device="cuda")
+    lse = torch.randn(3, 4, device="cuda")
+    lse[1, 0] = lse[0, 1] = -math.inf
+    lse[:, 2] = -math.inf
+    o[1, 3] = lse[1, 3] = math.nan
+    out, l = torch.empty(4, 64, device="cuda"), torch.empty(4, device="cuda")
+    L.eta_lse_merge(o, lse, out, l)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[3]).all() and torch.isnan(l[3])
+    assert torch.isfinite(out[:2]).all() and torch.isfinite(l[:2]).all()
+    assert torch.all(out[2] == 0) and l[2] == -math.inf
