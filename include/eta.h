@@ -613,9 +613,9 @@ eta_status_t eta_paged_decode(const eta_dims_t* dims, int32_t n_pages, const eta
  * The prefix of up to 256 (row, head) pairs of one KV head is one pass of tensor-core
  * tiles (S = Q K^T, O += P V, 128 keys each) over its keys; a row's own keys are a pass
  * of their own; all passes are cut into shares of equal cost, one per SM.  bf16 output:
- * the weights P are rounded to bf16 (a relative error of at most 2^-8, the output's own)
- * and the soft gate takes an approximate tanh (2^-11); fp32 output: P is the sum of
- * three bf16 terms (2^-24) and the gate an exponential and a division.
+ * the weights P are rounded to bf16 (a relative error of at most 2^-8, as the output's
+ * own rounding) in their product with V, not in their sum; fp32 output: P is the sum of three
+ * bf16 terms (2^-24).  lse is the same bits for both.
  * scale > 0 (0: 1 / sqrt(d)).
  * table, lengths, o_format, o, lse: as eta_paged_decode.
  * ws: eta_shared_decode_workspace_size(dims, n_groups) bytes, 16-byte aligned, no

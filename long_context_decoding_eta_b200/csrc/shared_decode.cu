@@ -466,9 +466,9 @@ ETA_DEV float ex2_approx(float x) {             // 2^x on the SFU; -inf gives 0
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-ETA_DEV float tanh_approx(float x) {
+ETA_DEV float rcp_approx(float x) {
   float y;
-  asm("tanh.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 ETA_DEV float fmax3(float a, float b, float c) {
@@ -531,22 +531,31 @@ ETA_DEV bool wait_issued(volatile int* issued, volatile int* end, int item,
 // The gate on 32 scores of a query row, in raw units (see the softmax).
 struct GateArgs {
   float tau_raw, ta, tb;
+  float zero;           // 0, or NaN where tau is
 };
-template <int GATE, int NS>
+template <int GATE>
 ETA_DEV void gate32(float* v, const GateArgs& g) {
   if constexpr (GATE == HARD) {
     // a selection: a flag times the score would make NaN of an infinite score
 #pragma unroll
     for (int u = 0; u < 32; ++u) v[u] = v[u] >= g.tau_raw ? v[u] : 0.f;
   } else if constexpr (GATE == SOFT) {
+    // s / (1 + e), e = 2^x: two keys share a reciprocal, 1 / b0 = b1 / (b0 b1).  x is at most
+    // 63, which keeps b0 b1 finite (s * 2^-63 stands for 0); the minimum also keeps a NaN (a
+    // key past the end) away from its neighbour.  s * 0 makes NaN of an infinite score, which
+    // the quotient would.
 #pragma unroll
-    for (int u = 0; u < 32; ++u) {
-      if constexpr (NS == 1) {
-        const float hs = 0.5f * v[u];
-        v[u] = fmaf(hs, tanh_approx(fmaf(v[u], g.ta, -g.tb)), hs);
-      } else {
-        v[u] = __fdividef(v[u], 1.f + ex2_approx(fmaf(v[u], g.ta, -g.tb)));   // 0 once 2^x is inf
-      }
+    for (int u = 0; u < 32; u += 2) {
+      const float2 s2 = make_float2(v[u], v[u + 1]);
+      const float2 x = __ffma2_rn(s2, make_float2(g.ta, g.ta), make_float2(-g.tb, -g.tb));
+      const float2 b = __fadd2_rn(make_float2(ex2_approx(fminf(x.x, 63.f)),
+                                              ex2_approx(fminf(x.y, 63.f))),
+                                  make_float2(1.f, 1.f));
+      const float r = rcp_approx(b.x * b.y);
+      const float2 w = __fmul2_rn(make_float2(b.y, b.x), make_float2(r, r));
+      const float2 y = __ffma2_rn(s2, w, __fmul2_rn(s2, make_float2(g.zero, g.zero)));
+      v[u] = y.x;
+      v[u + 1] = y.y;
     }
   }
 }
@@ -1053,18 +1062,20 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
                          ETA_IN_BOUNDS(h, p.Hq, p.status);
       const bool store = valid && (!s.check || p.ws.row[b].start > 0);   // the row shares
       // Gated logits in raw units u (the gated logit is scale * u), so that the scale
-      // folds into the constants: the hard gate keeps s iff s >= tau / scale; the soft
-      // gate is hs + hs * tanh(s * ta - tb), hs = s / 2, for a bf16 output (one
-      // transcendental a key, 2^-11 off, below the output's own rounding), and
-      // s / (1 + 2^(s * ta - tb)) for an fp32 one; and e^(scale * (u - m)) is
-      // 2^(u * c1 - m * c1), c1 = scale * log2(e).
+      // folds into the constants: the hard gate keeps s iff s >= tau / scale, the soft
+      // gate is s / (1 + 2^(s * ta - tb)), and e^(scale * (u - m)) is
+      // 2^(u * c1 - m * c1), c1 = scale * log2(e).  (s / 2 + s / 2 * tanh((s - tau) / 2T)
+      // with the approximate tanh takes one transcendental less, but it is off by up to
+      // 2^-12 |s|, in lse too, and that grows with the scores.  64 rows over 128K tokens,
+      // bf16: 153 us with it, 173 as it is, 189 with a reciprocal for every key.)
       GateArgs ga = {};
       if constexpr (GATE != NONE) {
         const float tau = valid ? p.tau[(size_t)b * p.Hq + h] : 0.f;
-        const float f = (NS == 1 ? 0.5f : -kLog2e) * p.invT;
+        const float f = -kLog2e * p.invT;
         ga.tau_raw = tau / p.scale;
         ga.ta = p.scale * f;
         ga.tb = tau * f;
+        ga.zero = isnan(tau) ? tau : 0.f;
       }
       float m = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
@@ -1106,8 +1117,8 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
             tmem_ld32(tSh + 32, sv + 32);
             tmem_wait_ld32(sv);
             tmem_wait_ld32(sv + 32);
-            gate32<GATE, NS>(sv, ga);
-            gate32<GATE, NS>(sv + 32, ga);
+            gate32<GATE>(sv, ga);
+            gate32<GATE>(sv + 32, ga);
             if (lim < SUB) {                     // keys past the end
 #pragma unroll
               for (int c = 0; c < SUB; ++c)

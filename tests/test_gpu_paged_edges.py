@@ -215,3 +215,64 @@ def test_merge_keeps_nan():
     assert torch.isnan(out[3]).all() and torch.isnan(l[3])
     assert torch.isfinite(out[:2]).all() and torch.isfinite(l[:2]).all()
     assert torch.all(out[2] == 0) and l[2] == -math.inf
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("form", ["paged", "shared"])
+def test_soft_gate_of_large_scores(form, out):
+    """Every key of a row is the same, so that lse = gated score + log n with nothing to
+    average the gate's error: scores of about 20, thresholds within 3 T of them."""
+    B, Hq, d, n = 48, 8, 64, 64 * 3 + 17
+    c = make_cache([n] * B, 1, d, 64, seed=3)
+    c.K.zero_()
+    c.K[..., 0] = 8.0                        # scale 1/8: the score is q[0]
+    c.table[:, :3] = c.table[0, :3]          # one shared prefix
+    q = torch.zeros(B, Hq, d)
+    q[..., 0] = torch.linspace(16.0, 23.0, Hq)
+    q = q.to(torch.bfloat16).cuda()
+    T = 8.0
+    tau = (q[..., 0].float() + torch.linspace(-24.0, 24.0, B, device="cuda")[:, None]).contiguous()
+    dec = PagedEtaDecoder(c, Hq, T=T, out_dtype=out)
+    if form == "paged":
+        o, lse = dec.decode(q, tau=tau, all_blocks=True)
+    else:
+        o, lse = dec.shared_decode(q, [0, B], [3 * 64], tau=tau)
+    dec.check_status()
+    p_eps = P_EPS[out] if form == "paged" else {torch.bfloat16: 2.0 ** -8}.get(out, 2.0 ** -24)
+    assert check(c, q, o, lse, tau, T, p_eps=p_eps, gate_eps=2.0 ** -20) == B * Hq
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [None, 0.0, 0.05, 2.0])
+def test_lse_is_the_same_for_both_output_types(T, d):
+    lens = [64 * 9 + 5, 64 * 9 + 64, 64 * 10 + 1, 90]
+    c = make_cache(lens, 2, d, 64, seed=17, poison=True)
+    c.table[1:3, :9] = c.table[0, :9]
+    gen = torch.Generator().manual_seed(6)
+    q = (4 * torch.randn(4, 8, d, generator=gen)).to(torch.bfloat16).cuda()
+    tau = (4 * torch.randn(4, 8, generator=gen)).cuda()
+    lse = []
+    for out in (torch.float32, torch.bfloat16):
+        dec = PagedEtaDecoder(c, 8, T=T, out_dtype=out)
+        dec.shared_decode(q, [0, 3, 4], [9 * 64, 0], tau=tau)
+        dec.check_status()
+        lse.append(dec.lse)
+    assert torch.isfinite(lse[0]).all() and torch.equal(*lse)
+
+
+def test_a_threshold_that_is_nan():
+    """A soft gate of a NaN threshold is NaN; other heads are as they were."""
+    c = make_cache([64 * 3 + 5] * 2, 1, 64, 64, seed=18)
+    c.table[1, :3] = c.table[0, :3]
+    q = torch.randn(2, 4, 64, generator=torch.Generator().manual_seed(9)).to(torch.bfloat16).cuda()
+    tau = torch.full((2, 4), 0.3, device="cuda")
+    dec = PagedEtaDecoder(c, 4, T=0.05)
+    o = dec.shared_decode(q, [0, 2], [3 * 64], tau=tau)[0].clone()
+    tau[1, 2] = math.nan
+    bad = torch.isnan(tau)
+    for call in (lambda: dec.decode(q, tau=tau, all_blocks=True),
+                 lambda: dec.shared_decode(q, [0, 2], [3 * 64], tau=tau)):
+        got, lse = call()
+        assert torch.isnan(got[bad]).all() and torch.equal(torch.isnan(lse), bad)
+        assert torch.isfinite(got[~bad]).all()
+    assert torch.equal(dec.o[~bad], o[~bad])
