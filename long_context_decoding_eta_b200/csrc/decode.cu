@@ -851,7 +851,8 @@ extern "C" eta_status_t eta_paged_decode(
 
   tc::TcParams prm = {};
   prm.Hq = dims->Hq; prm.Hkv = dims->Hkv; prm.T_max = dims->T_max; prm.NB = NB;
-  prm.blk = dims->blk; prm.scale = scale; prm.invT = T == 0.f ? -1.f : 1.f / T; prm.tau = tau;
+  prm.blk = dims->blk; prm.scale = scale; prm.tau = tau;
+  prm.invT = T == 0.f ? -1.f : inverse_temperature(T);
   prm.lengths = lengths; prm.union_idx = union_idx; prm.row_off = row_off;
   prm.cta_row = cta_row; prm.plan = plan; prm.part_o = part_o; prm.part_ml = part_ml;
   prm.status = dev_status; prm.R = R; prm.counts = union_cnt; prm.row_off_g = row_off;

@@ -2,6 +2,8 @@
 // layout of the bookkeeping array `state`.
 #pragma once
 
+#include <math.h>
+
 #include "eta_host.h"
 
 namespace eta {
@@ -32,5 +34,8 @@ inline eta_status_t check_pool(const eta_dims_t* d, int32_t n_pages) {
   if ((uint64_t)n_pages * d->Hkv * d->blk >= (1ull << 31)) return ETA_ERR_UNSUPPORTED;
   return ETA_OK;
 }
+
+// 1 / T of a soft gate, finite (and so 0 times it is 0) where T is too small for that.
+inline float inverse_temperature(float T) { return fminf(1.f / T, 2e38f); }
 
 }  // namespace eta

@@ -530,7 +530,7 @@ ETA_DEV bool wait_issued(volatile int* issued, volatile int* end, int item,
 
 // The gate on 32 scores of a query row, in raw units (see the softmax).
 struct GateArgs {
-  float tau_raw, ta, tb;
+  float tau_raw, tau, scale, f;
   float zero;           // 0, or NaN where tau is
 };
 template <int GATE>
@@ -547,7 +547,9 @@ ETA_DEV void gate32(float* v, const GateArgs& g) {
 #pragma unroll
     for (int u = 0; u < 32; u += 2) {
       const float2 s2 = make_float2(v[u], v[u + 1]);
-      const float2 x = __ffma2_rn(s2, make_float2(g.ta, g.ta), make_float2(-g.tb, -g.tb));
+      const float2 x = __fmul2_rn(
+          __ffma2_rn(s2, make_float2(g.scale, g.scale), make_float2(-g.tau, -g.tau)),
+          make_float2(g.f, g.f));
       const float2 b = __fadd2_rn(make_float2(ex2_approx(fminf(x.x, 63.f)),
                                               ex2_approx(fminf(x.y, 63.f))),
                                   make_float2(1.f, 1.f));
@@ -1063,18 +1065,19 @@ shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
       const bool store = valid && (!s.check || p.ws.row[b].start > 0);   // the row shares
       // Gated logits in raw units u (the gated logit is scale * u), so that the scale
       // folds into the constants: the hard gate keeps s iff s >= tau / scale, the soft
-      // gate is s / (1 + 2^(s * ta - tb)), and e^(scale * (u - m)) is
+      // gate is s / (1 + 2^((scale * s - tau) * f)), f = -log2(e) / T (the difference first:
+      // over a T near zero both terms are infinite), and e^(scale * (u - m)) is
       // 2^(u * c1 - m * c1), c1 = scale * log2(e).  (s / 2 + s / 2 * tanh((s - tau) / 2T)
       // with the approximate tanh takes one transcendental less, but it is off by up to
       // 2^-12 |s|, in lse too, and that grows with the scores.  64 rows over 128K tokens,
-      // bf16: 153 us with it, 173 as it is, 189 with a reciprocal for every key.)
+      // bf16: 153 us with it, 174 as it is, 189 with a reciprocal for every key.)
       GateArgs ga = {};
       if constexpr (GATE != NONE) {
         const float tau = valid ? p.tau[(size_t)b * p.Hq + h] : 0.f;
-        const float f = -kLog2e * p.invT;
         ga.tau_raw = tau / p.scale;
-        ga.ta = p.scale * f;
-        ga.tb = tau * f;
+        ga.tau = tau;
+        ga.scale = p.scale;
+        ga.f = -kLog2e * p.invT;
         ga.zero = isnan(tau) ? tau : 0.f;
       }
       float m = -INFINITY;
@@ -1515,7 +1518,7 @@ extern "C" eta_status_t eta_shared_decode(const eta_dims_t* dims, int32_t n_page
   sd::AttendParams a;
   a.B = dims->B; a.Hq = dims->Hq; a.Hkv = dims->Hkv; a.G = G; a.NB = pp.NB; a.blk = dims->blk;
   a.n_pages = n_pages; a.n_groups = n_groups; a.scale = scale;
-  a.invT = T > 0.f ? 1.f / T : 0.f;
+  a.invT = T > 0.f ? inverse_temperature(T) : 0.f;
   a.tau = tau; a.table = table; a.lengths = lengths; a.ws = wp; a.part_rows = L.part_rows;
   a.status = dev_status;
   const int gate = !tau ? sd::NONE : T == 0.f ? sd::HARD : sd::SOFT;

@@ -276,3 +276,32 @@ def test_a_threshold_that_is_nan():
         assert torch.isnan(got[bad]).all() and torch.equal(torch.isnan(lse), bad)
         assert torch.isfinite(got[~bad]).all()
     assert torch.equal(dec.o[~bad], o[~bad])
+
+
+@pytest.mark.parametrize("T", [1e-3, 1e-37, 1e-40])
+@pytest.mark.parametrize("form", ["paged", "shared"])
+def test_temperatures_near_zero(form, T):
+    """A vanishing temperature is the hard gate, and half the score where it meets tau
+    (zero keys and zero thresholds: 0)."""
+    c = make_cache([64 * 4 + 20, 64 * 4 + 33, 90], 1, 64, 64, seed=4)
+    c.table[1, :4] = c.table[0, :4]
+    c.K[c.table[2, 0].long()] = 0.0
+    q = torch.randn(3, 4, 64, generator=torch.Generator().manual_seed(8)).to(torch.bfloat16).cuda()
+    tau = torch.tensor([[0.5, 30.0, -30.0, 1.0], [0.2, 3e4, -3e4, 0.1], [0.0] * 4], device="cuda")
+    for out in (torch.float32, torch.bfloat16):
+        res = []
+        for t in (T, 0.0):
+            dec = PagedEtaDecoder(c, 4, T=t, out_dtype=out)
+            if form == "paged":
+                o, lse = dec.decode(q, tau=tau, all_blocks=True)
+            else:
+                o, lse = dec.shared_decode(q, [0, 2, 3], [4 * 64, 0], tau=tau)
+            dec.check_status()
+            res.append((o, lse))
+        (o, lse), (ho, hl) = res
+        assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+        if T < 1e-30:                        # no score is that near its threshold
+            n = check(c, q, ho, hl, tau, 0.0, p_eps=2.0 ** -8)
+            assert n >= 8
+            assert torch.allclose(o.float(), ho.float(), rtol=2.0 ** -7, atol=1e-5)
+            assert torch.allclose(lse, hl, atol=1e-5)
