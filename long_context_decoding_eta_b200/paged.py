@@ -19,6 +19,7 @@ Every step runs in libeta.so's kernels; this module only allocates and marshals.
 from __future__ import annotations
 
 import math
+import operator
 from typing import Optional
 
 import torch
@@ -26,13 +27,35 @@ import torch
 from . import _lib as L
 
 
+_INT32 = torch.iinfo(torch.int32)
+_INDEX_TYPES = (torch.int32, torch.int64, torch.int16, torch.int8, torch.uint8)
+
+
+def _whole(v) -> int:
+    if isinstance(v, bool) or (isinstance(v, torch.Tensor) and v.dtype not in _INDEX_TYPES):
+        raise ValueError(f"a whole number is wanted, not {v!r}")
+    try:
+        n = operator.index(v)
+    except TypeError:
+        raise ValueError(f"a whole number is wanted, not {v!r}") from None
+    if not _INT32.min <= n <= _INT32.max:
+        raise ValueError(f"{n} does not fit 32 bits")
+    return n
+
+
 def _index_tensor(x, device) -> torch.Tensor:
-    """int32 device tensor of a list, range or tensor of numbers."""
+    """int32 device tensor of a list, range or tensor of whole numbers.  A mask is none.
+    Numbers of an int64 tensor that do not fit become the ends of the int32 range, which
+    no row, page or length reaches, so that a call reports them and does not wrap them."""
     if isinstance(x, torch.Tensor):
         if x.dtype is torch.int32 and x.device == device and x.is_contiguous():
             return x
+        if x.dtype not in _INDEX_TYPES:
+            raise ValueError(f"rows, pages and lengths are whole numbers, not {x.dtype}")
+        if x.dtype is torch.int64:
+            x = x.clamp(_INT32.min, _INT32.max)
         return x.to(device=device, dtype=torch.int32).contiguous()
-    return torch.tensor(list(x), dtype=torch.int32, device=device)
+    return torch.tensor([_whole(v) for v in x], dtype=torch.int32, device=device)
 
 
 def _on(device, stream, fn, *args):

@@ -305,3 +305,28 @@ def test_temperatures_near_zero(form, T):
             assert n >= 8
             assert torch.allclose(o.float(), ho.float(), rtol=2.0 ** -7, atol=1e-5)
             assert torch.allclose(lse, hl, atol=1e-5)
+
+
+def test_types_of_index_tensors():
+    """A mask or a float names no rows; numbers past 32 bits are out of range, not wrapped."""
+    c = PagedKVCache(4, 1, 64, 64, 4, 12)
+    k = torch.randn(40, 1, 64).to(torch.bfloat16).cuda()
+    c.append(k, k, [0, 10, 20, 30, 40])
+    for bad in ([True, False, True, False], [1.0], [0.5], torch.tensor([True, False, True, False]),
+                torch.tensor([1.0]), torch.tensor([True] * 4, device="cuda"),
+                torch.zeros(2, device="cuda"), [1 << 31], [-(1 << 31) - 1]):
+        with pytest.raises(ValueError):
+            c.free(bad)
+    assert c.lengths.tolist() == [10] * 4
+    c.check_status()
+    for x in (torch.tensor([1 << 32]), torch.tensor([1 << 32], device="cuda"),
+              torch.tensor([-(1 << 32) + 1], device="cuda")):
+        c.free(x)
+        torch.cuda.synchronize()
+        assert int(c.dev_status) == L.DEVSTAT_BAD_ROW
+        c.dev_status.zero_()
+    assert c.lengths.tolist() == [10] * 4
+    for x in (torch.tensor([0]), torch.tensor([1], dtype=torch.int16, device="cuda"), (2,),
+              range(3, 4)):
+        c.free(x)
+    assert c.lengths.tolist() == [0] * 4
