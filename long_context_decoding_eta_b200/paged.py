@@ -14,6 +14,9 @@ decode over the admitted blocks) with the blocks behind the page table, and
 
 Every change of the bookkeeping is asynchronous on the current stream; nothing is
 read back to the host except by `check_status` and the read-only helpers that say so.
+Rows, pages, offsets and lengths are whole numbers: int32 device tensors go to the kernels
+as they are (a captured call takes no others), lists and host tensors are copied behind
+what the stream still runs, at some 10 us of host time each.
 Every step runs in libeta.so's kernels; this module only allocates and marshals.
 """
 from __future__ import annotations
@@ -35,12 +38,9 @@ def _whole(v) -> int:
     if isinstance(v, bool) or (isinstance(v, torch.Tensor) and v.dtype not in _INDEX_TYPES):
         raise ValueError(f"a whole number is wanted, not {v!r}")
     try:
-        n = operator.index(v)
+        return operator.index(v)
     except TypeError:
         raise ValueError(f"a whole number is wanted, not {v!r}") from None
-    if not _INT32.min <= n <= _INT32.max:
-        raise ValueError(f"{n} does not fit 32 bits")
-    return n
 
 
 def _index_tensor(x, device) -> torch.Tensor:
@@ -54,8 +54,22 @@ def _index_tensor(x, device) -> torch.Tensor:
             raise ValueError(f"rows, pages and lengths are whole numbers, not {x.dtype}")
         if x.dtype is torch.int64:
             x = x.clamp(_INT32.min, _INT32.max)
-        return x.to(device=device, dtype=torch.int32).contiguous()
-    return torch.tensor([_whole(v) for v in x], dtype=torch.int32, device=device)
+        x = x.to(torch.int32).contiguous()
+    else:
+        x = list(x)
+        if not set(map(type, x)) <= {int}:
+            x = [_whole(v) for v in x]
+        if x and not (_INT32.min <= min(x) and max(x) <= _INT32.max):
+            raise ValueError("a number does not fit 32 bits")
+        x = torch.tensor(x, dtype=torch.int32)
+    if x.device.type != "cpu" or device.type == "cpu":
+        return x.to(device)
+    if torch.cuda.is_current_stream_capturing():
+        raise ValueError("a captured call takes its rows, pages and lengths as device tensors: "
+                         "a copy of host numbers cannot be captured")
+    # from pinned memory, so that the copy does not wait for what the stream still runs; the
+    # pinned block is not used again before the copy is over
+    return x.pin_memory().to(device, non_blocking=True)
 
 
 def _on(device, stream, fn, *args):

@@ -330,3 +330,52 @@ def test_types_of_index_tensors():
               range(3, 4)):
         c.free(x)
     assert c.lengths.tolist() == [0] * 4
+
+
+def test_lists_do_not_wait_for_the_stream():
+    """Index lists reach the device behind the work that is on the stream already: the calls
+    return while it still runs."""
+    c = PagedKVCache(4, 1, 64, 64, 4, 12)
+    k = torch.randn(300, 1, 64).to(torch.bfloat16).cuda()
+    dec = PagedEtaDecoder(c, 2, T=None)
+    q = torch.randn(4, 2, 64).to(torch.bfloat16).cuda()
+
+    def calls():
+        c.append(k, k, [0, 200, 200, 200, 300])
+        c.fork([0, 0], [1, 2])
+        dec.shared_decode(q, [0, 3, 4], [192, 0])
+        c.copy_pages(torch.tensor([0]), torch.tensor([11]))
+        c.free(range(4))
+
+    calls()                                   # allocates, loads the kernels
+    torch.cuda.synchronize()
+    c.check_status()
+    done = torch.cuda.Event()
+    torch.cuda._sleep(2_000_000_000)          # about a second
+    calls()
+    done.record()
+    assert not done.query()
+    done.synchronize()
+    c.check_status()
+    dec.check_status()
+    assert int(c.n_free) == 12 and c.lengths.tolist() == [0] * 4
+
+
+def test_lists_are_refused_in_a_capture():
+    c = PagedKVCache(4, 1, 64, 64, 4, 12)
+    dec = PagedEtaDecoder(c, 2, T=None)
+    q = torch.zeros(4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    rows = torch.tensor([0], dtype=torch.int32, device="cuda")
+    host = rows.cpu()
+    c.free(rows)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.free(rows)
+        for call in (lambda: c.free([0]), lambda: c.fork([0], rows), lambda: c.free(host),
+                     lambda: dec.shared_decode(q, [0, 4], [0])):
+            with pytest.raises(ValueError, match="captur"):
+                call()
+    g.replay()
+    torch.cuda.synchronize()
+    c.check_status()
