@@ -608,7 +608,8 @@ eta_status_t eta_paged_decode(const eta_dims_t* dims, int32_t n_pages, const eta
  * prefix_len is rounded down to whole pages; a row shorter than that does not share
  * and is read by itself, as is every row of a group of one.  The page numbers of the
  * prefix come from the group's first row that is long enough: a row of the group whose
- * table holds other pages there gets the group's keys, not its own.  Rows of length 0
+ * table holds other pages there gets the group's keys, not its own (the checked build
+ * latches BAD_ROW for it).  Rows of length 0
  * give o = 0, lse = -inf; NaN and +inf scores as eta_decode.
  * The prefix of up to 256 (row, head) pairs of one KV head is one pass of tensor-core
  * tiles (S = Q K^T, O += P V, 128 keys each) over its keys; a row's own keys are a pass

@@ -126,8 +126,8 @@ struct Ws {
 };
 
 struct PlanParams {
-  int B, Hkv, G, NB, blk, n_groups, P;
-  const int32_t *lengths, *group_off, *prefix_len;
+  int B, Hkv, G, NB, blk, n_groups, n_pages, P;
+  const int32_t *lengths, *group_off, *prefix_len, *table;
   Ws ws;
   int32_t* status;
 };
@@ -202,6 +202,18 @@ __global__ void __launch_bounds__(kPlan) shared_plan_kernel(const PlanParams p) 
         if (min(p.lengths[r], cap) >= nb * p.blk) {
           p.ws.row[r].start = nb;
           p.ws.row[r].group = g;
+        }
+    if constexpr (kChecked)                      // the rows hold the pages that are read
+      if (share)
+        for (int r = first; r < r1; ++r) {
+          if (min(p.lengths[r], cap) < nb * p.blk) continue;
+          bool other = false;
+          for (int j = lane; j < nb; j += 32) {
+            const int page = p.table[(size_t)first * p.NB + j];   // out of range: BAD_BLOCK
+            other |= (unsigned)page < (unsigned)p.n_pages &&
+                     page != p.table[(size_t)r * p.NB + j];
+          }
+          if (other) set_status(p.status, ETA_DEVSTAT_BAD_ROW);
         }
     if (lane == 0) {
       GroupRec rec;
@@ -1510,8 +1522,8 @@ extern "C" eta_status_t eta_shared_decode(const eta_dims_t* dims, int32_t n_page
 
   sd::PlanParams pp;
   pp.B = dims->B; pp.Hkv = dims->Hkv; pp.G = G; pp.NB = num_blocks(dims); pp.blk = dims->blk;
-  pp.n_groups = n_groups; pp.P = P; pp.lengths = lengths; pp.group_off = group_off;
-  pp.prefix_len = prefix_len; pp.ws = wp; pp.status = dev_status;
+  pp.n_groups = n_groups; pp.n_pages = n_pages; pp.P = P; pp.lengths = lengths; pp.group_off = group_off;
+  pp.prefix_len = prefix_len; pp.table = table; pp.ws = wp; pp.status = dev_status;
   st = launch_k(sd::shared_plan_kernel, dim3(1), dim3(sd::kPlan), 0, s, pp);
   if (st != ETA_OK) return st;
 
