@@ -1,6 +1,7 @@
 """Calls at the edges of what the paged decodes take: shares without a single key, values
 that are not finite, thresholds and temperatures at the ends of their range, index lists."""
 import math
+import random
 
 import pytest
 import torch
@@ -379,3 +380,59 @@ def test_lists_are_refused_in_a_capture():
     g.replay()
     torch.cuda.synchronize()
     c.check_status()
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_hard_gated_lists_against_64_bits(out):
+    """How many heads are compared counts here: a head of n keys in its blocks is left out
+    for a near-tie with probability 0.4 n 4 ds at most (scores of density 0.4, ds = 132 *
+    2^-24 * 10), 0.12 for the longest list and 0.04 on average; four in five is far below."""
+    lens = [1500, 130, 64, 0, 900, 333]
+    Hq, Hkv, d, blk = 16, 4, 128, 64
+    c = make_cache(lens, Hkv, d, blk, seed=23, poison=True)
+    rng = random.Random(5)
+    dec = PagedEtaDecoder(c, Hq, T=0.0, out_dtype=out)
+    blocks = []
+    for b, n in enumerate(lens):
+        nb = -(-n // blk)
+        row = [sorted(rng.sample(range(nb), rng.randint(min(1, nb), nb))) for _ in range(Hkv)]
+        for g in range(Hkv):
+            dec.union_idx[b, g, :len(row[g])] = torch.tensor(row[g], dtype=torch.int32).cuda()
+            dec.union_cnt[b, g] = len(row[g])
+        blocks.append(row)
+    gen = torch.Generator().manual_seed(24)
+    q = torch.randn(len(lens), Hq, d, generator=gen).to(torch.bfloat16).cuda()
+    tau = (0.3 + 0.5 * torch.randn(len(lens), Hq, generator=gen)).cuda()
+    o, lse = dec.decode(q, tau=tau)
+    dec.check_status()
+    assert check(c, q, o, lse, tau, 0.0, blocks, p_eps=P_EPS[out]) >= 0.8 * 5 * Hq
+
+
+def test_hard_gate_after_fork_free_and_compact():
+    """Both decodes of rows that were appended, forked, freed, compacted and forked again;
+    near-ties as above, 420 keys a row: 0.03 a head."""
+    B, Hq, Hkv, d, blk = 6, 8, 2, 128, 64
+    c = PagedKVCache(B, Hkv, d, blk, 12, 40)
+    gen = torch.Generator().manual_seed(25)
+
+    def tokens(n):
+        return [torch.randn(n, Hkv, d, generator=gen).to(torch.bfloat16).cuda() for _ in range(2)]
+
+    n0 = 5 * blk + 17
+    c.append(*tokens(n0 + 100), [0, n0, n0, n0, n0, n0 + 100, n0 + 100])
+    c.fork([0, 0, 0], [1, 2, 3])
+    c.append(*tokens(200), [0, 40, 80, 120, 160, 200, 200])
+    c.free([0, 4])
+    c.compact()
+    c.fork([2], [0])
+    c.append(*tokens(4), [0, 1, 2, 3, 4, 4, 4])
+    q = torch.randn(B, Hq, d, generator=gen).to(torch.bfloat16).cuda()
+    tau = (0.3 + 0.5 * torch.randn(B, Hq, generator=gen)).cuda()
+    dec = PagedEtaDecoder(c, Hq, T=0.0)
+    assert c.lengths.tolist() == [n0 + 41] * 4 + [0, 0]
+    for call in (lambda: dec.shared_decode(q, [0, 4, 6], [n0, 0], tau=tau),
+                 lambda: dec.decode(q, tau=tau, all_blocks=True)):
+        o, lse = call()
+        c.check_status()
+        dec.check_status()
+        assert check(c, q, o, lse, tau, 0.0, p_eps=2.0 ** -24) >= 0.8 * 4 * Hq
