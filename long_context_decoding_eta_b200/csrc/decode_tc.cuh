@@ -280,8 +280,8 @@ ETA_DEV void plan_local(const int32_t* counts, int R, int NB, int* row_off, Fuse
 // 64-dim half stays zero, so those accumulator rows are zero and not written out).
 // PAGED: K and V are page pools [n_pages, Hkv, blk, d] behind p.table, every block of a
 // row is taken when p.union_idx is NULL, and DENSE means "no gate" alone.
-// NS: the bf16 terms that P is the sum of, in NS * G columns of P^T (2: 2^-18 relative;
-// 3: 2^-27, below the rounding of fp32 itself).
+// NS: the bf16 terms that P is the sum of, in NS * G columns of P^T (2: 2^-16 relative;
+// 3: 2^-24, the rounding of fp32 itself).
 template <int G, bool DENSE, bool LOCAL, bool FLAGS, bool PDL_IN = false, bool PLAN_IN = false,
           int DD = 128, bool PAGED = false, int NS = 2>
 ETA_DEV void decode_tc_body(unsigned char* smem, const CUtensorMap* tmK, const CUtensorMap* tmV,

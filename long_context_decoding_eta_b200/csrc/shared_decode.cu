@@ -615,9 +615,10 @@ struct Tm {
   static_assert(NS * 32 <= (S_HALF ? S_HALF : S_STREAM), "P terms");
 };
 
-// GATE: Gate.  NS: the bf16 terms of P.  One (2^-9) for a bf16 output, whose own rounding
-// is the same; three (2^-27) for an fp32 one, where two (2^-18) left an error of 2e-6, eight
-// times the plain fp32 form's.
+// GATE: Gate.  NS: the bf16 terms of P, each half a step of 8 bits behind the one before.  One
+// (2^-8) for a bf16 output, whose own rounding is as coarse: the largest error is then 1.4 times
+// that of fp32 weights (2.3e-3 and 1.65e-3, 64 rows over 128K tokens).  Three (2^-24) for an
+// fp32 one, where two (2^-16) left an error of 2e-6, eight times the plain fp32 form's.
 template <int D, int GATE, int NS>
 __global__ void __launch_bounds__(NT, 1)
 shared_attend_kernel(const __grid_constant__ CUtensorMap tmQ,
