@@ -584,7 +584,8 @@ typedef enum { ETA_OUT_F32 = 0, ETA_OUT_BF16 = 1 } eta_out_format_t;
  * eta_decode (prune, vsum and cnt included).  Always the tensor-core engine
  * (eta_set_decode_engine does not apply), with the weights as the sum of two bf16 terms
  * (2^-16) for a bf16 output and of three (2^-24) for an fp32 one.
- * ws: eta_decode_workspace_size(dims) bytes.
+ * ws: eta_decode_workspace_size(dims) bytes.  Limit (else ETA_ERR_UNSUPPORTED):
+ * B * Hkv * NB < 2^30.
  * dev_status: TIMEOUT, BAD_LENGTH, BAD_BLOCK (a block past the row's length, or a page
  * out of range: skipped).
  */

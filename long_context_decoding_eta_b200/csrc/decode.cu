@@ -810,6 +810,9 @@ extern "C" eta_status_t eta_paged_decode(
     int32_t* dev_status, void* stream) {
   eta_status_t st = check_pool(dims, n_pages);
   if (st != ETA_OK) return st;
+  // the shares are cut from a 32-bit sum of every pair's blocks; rows that share pages can
+  // have more of them than the pool
+  if ((uint64_t)dims->B * dims->Hkv * num_blocks(dims) >= (1ull << 30)) return ETA_ERR_UNSUPPORTED;
   if (!q || !K_pool || !V_pool || !table || !lengths || !o || !lse) return ETA_ERR_INVALID_ARG;
   if (!aligned16(K_pool) || !aligned16(V_pool) || !aligned16(q)) return ETA_ERR_INVALID_ARG;
   if (o_format != ETA_OUT_F32 && o_format != ETA_OUT_BF16) return ETA_ERR_INVALID_ARG;

@@ -1,8 +1,12 @@
-"""What the paged layer takes for rows, pages, offsets and lengths."""
+"""What the paged layer takes for rows, pages, offsets and lengths, and the sizes that the
+paged decode refuses (on the host, before anything is launched)."""
+import ctypes as C
+
 import numpy as np
 import pytest
 import torch
 
+from long_context_decoding_eta_b200 import _lib as L
 from long_context_decoding_eta_b200.paged import _index_tensor
 
 CPU = torch.device("cpu")
@@ -37,3 +41,13 @@ def test_empty_and_passed_through():
 def test_wide_numbers_do_not_wrap():
     x = torch.tensor([1 << 32, (1 << 32) + 1, -(1 << 32), 7])
     assert _index_tensor(x, CPU).tolist() == [2 ** 31 - 1, 2 ** 31 - 1, -2 ** 31, 7]
+
+
+@pytest.mark.parametrize("B,code", [(8192, 2), (4096, 2), (4095, 3)])
+def test_paged_decode_refuses_more_blocks_than_32_bits_count(B, code):
+    """Rows that share pages can have 2^30 and more blocks in all; just below, the call
+    goes on to its next check (a missing workspace)."""
+    dims, fake = L.Dims.of(B, 8, 4, 64, 64, 65536 * 64), C.c_void_p(4096)
+    assert L.lib().eta_paged_decode(C.byref(dims), 13, fake, None, fake, fake, fake, fake, None,
+                                    None, 0.0, 0.0, 0, None, None, 0, fake, fake, None, 0, None,
+                                    None) == code
