@@ -7,8 +7,8 @@
 // not matter.  The data kernels move whole 16-byte vectors and are bound by HBM (read +
 // write of the moved tokens), the bookkeeping by launch latency.  So append, fork and free
 // are one launch each: every CTA works the whole decision out for itself (a scan over the
-// rows or pairs, 1,024 at most), and what it was read from, the lengths and the free
-// count, is written by the CTA that finishes last.  Above 1,024 rows a plan kernel of one
+// rows or pairs), and what it was read from, the lengths and the free count, is written by
+// the CTA that finishes last.  Above 1,024 rows, or 64 forked pairs, a plan kernel of one
 // CTA decides for all.  Measured (us a launch, replayed): append of 64 rows, 11,000 tokens of
 // 2 KB, 9.9 (read + write 4.6 TB/s); free and fork of 6 rows 6.5 and 5.4, of 56 rows of 300 pages 11.5 and
 // 7.7; compaction of 2.06 GB 333 (6.2 TB/s), of 34 MB 13; 1,777 pages of 128 KB 84 (5.5 TB/s).
@@ -22,7 +22,12 @@ namespace pg {
 
 constexpr int kPlan = 1024;       // threads of a one-CTA plan
 constexpr int kCopy = 256;        // threads of a data-moving CTA
-constexpr int kLocal = 1024;      // rows up to which every CTA plans by itself
+// Up to kLocal rows every CTA of an append plans by itself (us: 64 rows 5.2, with a plan launch
+// 7.2; 512 rows 6.8 and 7.8; 1,024 rows 8.2 and 8.6), up to kLocalPairs pairs every CTA of a fork,
+// of which there are 8 a pair (4 pairs 5.4 and 6.2; 64 pairs 6.4 and 6.4; 96 pairs 6.8 and 6.4;
+// 256 pairs 14.2 and 7.6).
+constexpr int kLocal = 1024;
+constexpr int kLocalPairs = 64;
 constexpr int kChunk = 4096;      // pages per CTA of the compaction's scan
 constexpr int kOwnCount = 8;      // chunks up to which every such CTA counts by itself
 constexpr int kOwnCheck = 2048;   // pairs up to which every copying CTA checks them by itself
@@ -310,8 +315,8 @@ __global__ void __launch_bounds__(kCopy)
 fork_kernel(const Pool p, const int32_t* __restrict__ src, const int32_t* __restrict__ dst,
             int n, const int2* plan_g, int32_t* done) {
   ETA_PDL_ENTRY();
-  __shared__ int2 s_rec[LOCAL ? kLocal : 1];
-  __shared__ int32_t s_first[LOCAL ? kLocal : 1];
+  __shared__ int2 s_rec[LOCAL ? kLocalPairs : 1];
+  __shared__ int32_t s_first[LOCAL ? kLocal : 1];      // by row
   const int i = blockIdx.x;
   int2 fr = make_int2(0, 0);
   const int2* rec = plan_g;
@@ -863,7 +868,7 @@ extern "C" eta_status_t eta_page_fork(const eta_dims_t* dims, int32_t n_pages, i
   int2* rec = at<int2>(ws, w.rec);
   int32_t* done = at<int32_t>(ws, w.done);
   const dim3 grid(n, 8);
-  if (dims->B <= kLocal)
+  if (dims->B <= kLocal && n <= kLocalPairs)
     return launch_k(fork_kernel<true>, grid, dim3(kCopy), 0, s, p, src, dst, (int)n,
                     (const int2*)nullptr, done);
   st = launch_k(fork_plan_kernel, dim3(1), dim3(kPlan), 0, s, p, src, dst, (int)n,
