@@ -11,7 +11,7 @@
 // the CTA that finishes last.  Above 1,024 rows, or 64 forked pairs, a plan kernel of one
 // CTA decides for all.  Measured (us a launch, replayed): append of 64 rows, 11,000 tokens of
 // 2 KB, 9.9 (read + write 4.6 TB/s); free and fork of 6 rows 6.5 and 5.4, of 56 rows of 300 pages 11.5 and
-// 7.7; compaction of 2.06 GB 333 (6.2 TB/s), of 34 MB 13; 1,777 pages of 128 KB 84 (5.5 TB/s).
+// 7.7; compaction of 2.06 GB 333 (6.2 TB/s), of 34 MB 13; 1,777 pages of 128 KB 79 (5.9 TB/s).
 #include <algorithm>
 
 #include "eta_common.cuh"
@@ -30,7 +30,11 @@ constexpr int kLocal = 1024;
 constexpr int kLocalPairs = 64;
 constexpr int kChunk = 4096;      // pages per CTA of the compaction's scan
 constexpr int kOwnCount = 8;      // chunks up to which every such CTA counts by itself
-constexpr int kOwnCheck = 2048;   // pairs up to which every copying CTA checks them by itself
+// Copies of at most kOwnCheck pairs and kOwnBytes, read and written once, are checked by every
+// copying CTA by itself (us: 2,048 pairs of 16 KB, K and V, 11.8, with a plan launch 15.6; 1,024
+// pairs of 128 KB 46.9 and 47.0; 1,777 of them 84.4 and 78.5; 2,048 of them 95.3 and 89.1).
+constexpr int kOwnCheck = 2048;
+constexpr int64_t kOwnBytes = 1 << 27;
 
 struct Pool {
   int B, NB, n_pages, Hkv, blk, d;
@@ -655,7 +659,7 @@ copy_plan_kernel(const Pool p, const int32_t* __restrict__ src, const int32_t* _
     if (page_ok(p, src[i])) mark[src[i]] = -1;
 }
 
-// OWN: few pairs of a small pool, every CTA checks them all by itself before it copies,
+// OWN: few pairs and bytes of a small pool, every CTA checks them all by itself before it copies,
 // with a bit a page in the ring's memory; else mark is copy_plan_kernel's.
 template <int CH, bool OWN>
 __global__ void __launch_bounds__(kMove)
@@ -938,10 +942,10 @@ extern "C" eta_status_t eta_page_copy(const eta_dims_t* dims, int32_t n_pages, e
   int32_t* mark = at<int32_t>(ws, w.rank);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool wide = wide_chunks(dims);
-  const int64_t chunks = (int64_t)n * 2 * dims->Hkv * dims->blk * dims->d * 2 / 8192;
-  const dim3 grid(copy_grid(chunks, kMovePerSm));
+  const int64_t bytes = (int64_t)n * 2 * dims->Hkv * dims->blk * dims->d * 2;
+  const dim3 grid(copy_grid(bytes / 8192, kMovePerSm));
   const int32_t* no_mark = nullptr;
-  if (n <= kOwnCheck && n_pages <= kRing * 8)
+  if (n <= kOwnCheck && bytes <= kOwnBytes && n_pages <= kRing * 8)
     return wide ? launch_move<copy_kernel<16384, true>>(grid, s, p, src, dst, (int)n, no_mark)
                 : launch_move<copy_kernel<8192, true>>(grid, s, p, src, dst, (int)n, no_mark);
   if ((st = launch_k(copy_plan_kernel, dim3(1), dim3(kPlan), 0, s, p, src, dst, (int)n, mark)) !=
