@@ -29,7 +29,11 @@ constexpr int kCopy = 256;        // threads of a data-moving CTA
 constexpr int kLocal = 1024;
 constexpr int kLocalPairs = 64;
 constexpr int kChunk = 4096;      // pages per CTA of the compaction's scan
-constexpr int kOwnCount = 8;      // chunks up to which every such CTA counts by itself
+// Up to kOwnCount chunks every CTA of the scan counts all of the pool by itself.  A compaction
+// is then two launches instead of three, 12.3 us of the host's time instead of 14.0, for 0.2
+// to 0.6 us more of the GPU's (1,024 pages with nothing to move 8.0 us, with a count launch 7.6;
+// 16,384 pages 8.2 and 7.6; 32,768 pages 8.4 and 8.0, and 50.4 and 50.5 moving a quarter).
+constexpr int kOwnCount = 8;
 // Copies of at most kOwnCheck pairs and kOwnBytes, read and written once, are checked by every
 // copying CTA by itself (us: 2,048 pairs of 16 KB, K and V, 11.8, with a plan launch 15.6; 1,024
 // pairs of 128 KB 46.9 and 47.0; 1,777 of them 84.4 and 78.5; 2,048 of them 95.3 and 89.1).
@@ -541,10 +545,11 @@ __global__ void __launch_bounds__(kPlan) compact_plan_kernel(const Pool p, const
 //
 // A page's K and V are copied in chunks of CH bytes through a ring of S stages in shared
 // memory, by bulk copies that one thread of the CTA issues: loads run S/2 chunks ahead of
-// the stores.  2 CTAs an SM, 64 KB each.  Bound by HBM, read + write: 2.06 GB in 318 us
-// (6,480 GB/s; the device's own copy of as much 313 us).  Loads and stores of 16 bytes a
-// thread reached 334 to 359 us over 2 to 8 CTAs of 256 threads an SM and 4 or 8 vectors
-// a thread, 32 KB chunks (6 stages, 1 CTA an SM) 319 us, 8 KB ones 344 to 392 us.
+// the stores.  2 CTAs an SM, 64 KB each.  Bound by HBM, read + write: a compaction of 2.06 GB
+// takes 333 us with its scan and tables (6.2 TB/s).  The copies alone, in a program of their
+// own: 318 us (6,480 GB/s; the device's own copy of as much 313 us), loads and stores of 16
+// bytes a thread 334 to 359 us over 2 to 8 CTAs of 256 threads an SM and 4 or 8 vectors a
+// thread, 32 KB chunks (6 stages, 1 CTA an SM) 319 us, 8 KB ones 344 to 392 us.
 constexpr int kMove = 128;        // threads: thread 0 copies, the others do the bookkeeping
 constexpr int kMovePerSm = 2;
 constexpr int kRing = 65536;
@@ -556,8 +561,8 @@ struct Ring {
 };
 
 // One thread: chunks blockIdx, blockIdx + grid, ... of `n` page copies, so that the chunks
-// in flight are neighbours (a page's chunks by neighbouring CTAs measured 80 us for 1,777
-// scattered pages of 128 KB, whole pages by a CTA 93 us).  pair(i, from, to) names copy i
+// in flight are neighbours (1,777 scattered pages of 128 KB, the copies alone: 80 us, whole
+// pages by a CTA 93 us).  pair(i, from, to) names copy i
 // and says whether it is made.
 template <int CH, int S, typename Pair>
 ETA_DEV void copy_ring(const Pool& p, int n, unsigned char* smem, Ring<S>* ring, Pair pair) {
