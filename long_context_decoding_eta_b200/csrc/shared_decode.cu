@@ -74,6 +74,11 @@ enum Gate { NONE = 0, HARD = 1, SOFT = 2 };
 // seg + t * cost; a CTA has the tiles that begin in its share of the costs.  With few
 // tiles every tile costs 1, so that they spread over all CTAs: 4 rows of 2,048 + 64 tokens
 // are 80 tiles for 80 CTAs, where the costs above left 44 of them three each.
+// The same costs serve every form; of {pair, single, own, seg} = {4, 3, 3, 4}, {4, 2, 2, 4},
+// {4, 4, 4, 4} and {1, 1, 1, 0} they are best or close to it, but for soft gates (us, 64 rows of
+// 16 / 4 heads of 128: one group of 128K tokens, bf16, no gate 103, 112, 107, 103; 32 groups of
+// one page and 4,096 own tokens, fp32, no gate 129, 134, 128, 128; four groups of up to 32K
+// tokens, bf16, no gate 90, 90, 104, 103; the same in fp32 with a soft gate 215, 180, 266, 253).
 struct Costs {
   int pair, single, own, seg;
   ETA_DEV int own_begin(int t) const { return t ? seg + t * own : 0; }
