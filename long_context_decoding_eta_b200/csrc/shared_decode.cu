@@ -30,7 +30,7 @@
 //   shared_combine_kernel  joins the parts of every (row, head).
 //
 // 64 rows of 16 / 4 heads of 128 over a 128K-token prefix and up to 1,024 own tokens each,
-// bf16 output: 121 us a call with new inputs (105 as a replayed graph, part of the keys in
+// bf16 output: 114 us a call with new inputs (103 as a replayed graph, part of the keys in
 // L2) for a floor of 52 (341 MB); the attend kernel alone runs at 45% of HBM, 47% of the
 // tensor pipe and 46% of the SFU, bound by the chain Q K^T - softmax - P V of its streams.
 // 4 rows of 2,048 + 64 tokens: 23 us, three launches' latency.

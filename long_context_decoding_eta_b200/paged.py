@@ -262,8 +262,10 @@ class PagedEtaDecoder:
             self.vardim = torch.zeros(B, Hkv, d, NB, dtype=f32, device=dev)
 
     def build_meta(self, blk_begin: int = 0, blk_end: int = -1, stream=None):
-        """Block metadata of blocks [blk_begin, blk_end) of every row (call it after a
-        prefill, a fork or a free; append_update after a decode step's append)."""
+        """Block metadata of blocks [blk_begin, blk_end) of every row.  Screening knows
+        these alone, not the lengths or the table: call it after an append of more than
+        one token, a fork or a free, over the blocks that changed (append_update after a
+        decode step's append).  It reads every key of those blocks."""
         c = self.cache
 
         def call():
